@@ -65,6 +65,19 @@ typedef enum moe_act {
     MOE_ACT_RELU2 = 1    /* h = max(x W1^T, 0)^2; W13 has I rows */
 } moe_act;
 
+/* Element type of the layer norm's tensors. */
+typedef enum moe_type {
+    MOE_TYPE_BF16 = 0,
+    MOE_TYPE_F32 = 1
+} moe_type;
+
+/* How a weight gradient is stored (the sums are FP32 either way). */
+typedef enum moe_wgrad {
+    MOE_WGRAD_BF16 = 0,    /* dw = bf16(sum) */
+    MOE_WGRAD_F32 = 1,     /* dw = sum, FP32 */
+    MOE_WGRAD_F32_ADD = 2  /* dw += sum, FP32: gradient accumulation */
+} moe_wgrad;
+
 /* Shape of one layer call.
  *   tokens T >= 1; hidden H, multiple of 8; experts E in [1, 1024];
  *   top_k k in [1, min(E, 32)]; inter I, multiple of 8 (expert intermediate);
@@ -340,6 +353,117 @@ MOE_API moe_status moe_ep_plan(int32_t experts, int32_t world, int32_t rank, int
                                const int32_t* counts_all, int32_t* send_offsets, int32_t* recv_offsets,
                                int32_t* recv_slot, int32_t* peer_send, int32_t* peer_recv);
 
+/* ---- Training ---------------------------------------------------------------
+ * The forward chain is layer norm -> gate -> route -> dispatch ->
+ * moe_expert_up_train -> moe_expert_down -> moe_combine; the calls below are the
+ * layer norm, the up projection that keeps what its gradient needs, and the
+ * gradients.  The library's conventions hold: contiguous row-major buffers of the
+ * caller, 16-byte aligned, work enqueued on `stream`, nothing allocated.  No
+ * gradient is summed with atomics: results do not change from run to run. */
+
+/* Layer norm over rows of `hidden` elements (any width from 1 to 2^20):
+ *   y = (x - mean) * rstd * gamma + beta,  rstd = 1 / sqrt(var + eps),
+ * var the mean of the centred squares; statistics in FP32, y rounded once.
+ *   type, wtype  moe_type of x and y, and of gamma and beta
+ *   x, y         device [rows, hidden] (y may alias x); rows >= 0 (with no rows
+ *                nothing is launched and x, y, mean, rstd may be NULL)
+ *   gamma, beta  device [hidden]
+ *   eps          >= 0, finite
+ *   mean, rstd   device f32 [rows] out, each may be NULL */
+MOE_API moe_status moe_layernorm(int64_t rows, int32_t hidden, int32_t type, int32_t wtype, const void* x,
+                                 const void* gamma, const void* beta, float eps, void* y, float* mean, float* rstd,
+                                 void* stream);
+
+/* Gradient of moe_layernorm.  With a = dy * gamma and xhat = (x - mean) * rstd:
+ *   dx     = rstd * (a - mean_c(a) - xhat * mean_c(a * xhat)) + dres
+ *   dgamma = sum over rows of dy * xhat,  dbeta = sum over rows of dy  (FP32)
+ *   dy, x      device [rows, hidden] of `type`; mean, rstd device f32 [rows]
+ *   dres       device [rows, hidden] of `type` or NULL: the residual branch's
+ *              gradient, added before the one rounding
+ *   dx         device [rows, hidden] out (may alias dy, x or dres)
+ *   dgamma, dbeta  device f32 [hidden] out (zeros when rows == 0)
+ *   scratch    device, 256-byte aligned, moe_layernorm_scratch_size bytes; its
+ *              contents on entry do not matter */
+MOE_API moe_status moe_layernorm_scratch_size(int64_t rows, int32_t hidden, size_t* bytes);
+MOE_API moe_status moe_layernorm_backward(int64_t rows, int32_t hidden, int32_t type, int32_t wtype, const void* dy,
+                                          const void* x, const void* gamma, const float* mean, const float* rstd,
+                                          const void* dres, void* dx, float* dgamma, float* dbeta, void* scratch,
+                                          size_t scratch_bytes, void* stream);
+
+/* Gradient of moe_combine (the shared term's and the residual's gradients are
+ * dout itself):
+ *   dy_perm[dest[p]] = bf16(topk_w[p] * dout[p / k])
+ *   dtopk_w[p]       = sum_c dout[p / k][c] * y_perm[dest[p]][c]   (FP32)
+ *   dout device bf16 [T, H]; y_perm device bf16 [T*k, H] as moe_combine took it
+ *   (may be NULL without dtopk_w); dest, topk_w as moe_combine took them;
+ *   dy_perm device bf16 [T*k, H] out: rows no pair points at are not written
+ *   (may alias y_perm: each element is read before it is written);
+ *   dtopk_w device f32 [T, k] out, 0 for an invalid pair, or NULL (fixed weights). */
+MOE_API moe_status moe_combine_backward(const moe_shape* shape, const uint16_t* dout, const uint16_t* y_perm,
+                                        const int32_t* dest, const float* topk_w, uint16_t* dy_perm, float* dtopk_w,
+                                        void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_dispatch's row copy:
+ *   dx[t] = bf16( sum_{j<k} dx_perm[dest[t*k+j]] + add[t] )
+ * summed in FP32 in j order, then `add` (device bf16 [T, H] or NULL: what reaches
+ * x another way -- the gate projection, shared experts; dx may alias it).  Pairs
+ * with dest < 0 are skipped.  dx_perm device bf16 [T*k, H]; dx device bf16 [T, H] out. */
+MOE_API moe_status moe_dispatch_backward(const moe_shape* shape, const uint16_t* dx_perm, const int32_t* dest,
+                                         const uint16_t* add, uint16_t* dx, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_route: dlogits[t][topk_ids[t,j]] = w_j (dw_j - sum_i w_i dw_i),
+ * with w = topk_w as moe_route returned it and dw = dtopk_w; 0 for every expert
+ * not selected.  dlogits device f32 [T, E] out.
+ * Device error: MOE_ERR_INVALID_ROUTE for an id out of range or repeated inside
+ * its token (the first counts, as in moe_dispatch); such a pair takes no part. */
+MOE_API moe_status moe_route_backward(const moe_shape* shape, const int32_t* topk_ids, const float* topk_w,
+                                      const float* dtopk_w, float* dlogits, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_route_sigmoid: with s = sigmoid(logit), p_j = s_j / sum_i s_i
+ * over the selection, dlogits[t][topk_ids[t,j]] =
+ * route_scale * p_j (1 - s_j) (dw_j - sum_i p_i dw_i), 0 elsewhere (the bias only
+ * selects and has no gradient).  logits, topk_ids, route_scale as in the forward
+ * call; device errors as moe_route_backward. */
+MOE_API moe_status moe_route_sigmoid_backward(const moe_shape* shape, const float* logits, const int32_t* topk_ids,
+                                              float route_scale, const float* dtopk_w, float* dlogits, void* ws,
+                                              size_t ws_bytes, void* stream);
+
+/* moe_expert_up that also keeps its pre-activations (no shared experts):
+ *   pre device bf16 [T*k, up] out: bf16(x_perm W13[e]^T), FP32 accumulation
+ *   h   device bf16 [T*k, I]  out: bf16(act(pre)), from the rounded pre
+ * rows past offsets[E] are not written.  Host error: MOE_ERR_UNSUPPORTED when
+ * shape->shared > 0 (here and in the two calls below); a shared expert trains as
+ * a shape of one expert whose bucket holds every token. */
+MOE_API moe_status moe_expert_up_train(const moe_shape* shape, const uint16_t* x_perm, const int32_t* offsets,
+                                       const uint16_t* w13, uint16_t* pre, uint16_t* h, void* ws, size_t ws_bytes,
+                                       void* stream);
+
+/* Gradient of the down projection and of the activation before it.  For the rows
+ * r of expert e, with dh = dy_perm[r] W2[e] (FP32 accumulation):
+ *   SwiGLU: dpre[r] = bf16([ dh u s (1 + g (1 - s)) | dh g s ]), (g | u) = pre[r],
+ *           s = sigmoid(g);   ReLU^2: dpre[r] = bf16(dh * 2 max(pre[r], 0))
+ *   dw2[e] = sum_r dy_perm[r]^T h[r], FP32 accumulation, stored as `wgrad` says
+ *   dy_perm device bf16 [T*k, H]; pre, h as moe_expert_up_train wrote them
+ *   dpre device bf16 [T*k, up] out (rows past offsets[E] not written), or NULL:
+ *        w2 and pre are then not read
+ *   dw2  device [E, H, I] out, bf16 or f32, or NULL: h is then not read.  An expert
+ *        without rows gets zeros (MOE_WGRAD_F32_ADD leaves it as it is).
+ * Host error: MOE_ERR_INVALID_ARG when both outputs are NULL. */
+MOE_API moe_status moe_expert_down_backward(const moe_shape* shape, const uint16_t* dy_perm, const int32_t* offsets,
+                                            const uint16_t* w2, const uint16_t* pre, const uint16_t* h,
+                                            uint16_t* dpre, void* dw2, int32_t wgrad, void* ws, size_t ws_bytes,
+                                            void* stream);
+
+/* Gradient of the up projection:
+ *   dx_perm[r] = bf16(dpre[r] W13[e]);  dw13[e] = sum_r dpre[r]^T x_perm[r]
+ *   dx_perm device bf16 [T*k, H] out (rows past offsets[E] not written), or NULL:
+ *           w13 is then not read
+ *   dw13    device [E, up, H] out, or NULL (x_perm is then not read); stored, and
+ *           filled for an expert without rows, as dw2 above. */
+MOE_API moe_status moe_expert_up_backward(const moe_shape* shape, const uint16_t* dpre, const int32_t* offsets,
+                                          const uint16_t* x_perm, const uint16_t* w13, uint16_t* dx_perm, void* dw13,
+                                          int32_t wgrad, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, return in *device_status the largest status code raised
  * by kernels on this workspace since the last read, and clear it (together
  * with the timeout site below). */
@@ -369,7 +493,8 @@ MOE_API moe_status moe_workspace_set_wait(void* ws, size_t ws_bytes, uint64_t lo
 /* Synchronise `stream` and return in *site where the last bounded wait that
  * ran out on this workspace gave up: 0 none, 1 the count kernel's look-back,
  * 2 a GEMM TMA producer, 3 a GEMM MMA issuer, 4 a GEMM epilogue, 5 the
- * small-row GEMM, 6 moe_layer's fused decode FFN.  Read it before
+ * small-row GEMM, 6 moe_layer's fused decode FFN, 7 / 8 / 9 a gradient GEMM's
+ * producer / MMA issuer (or its fixer warp) / epilogue.  Read it before
  * moe_status_read, which clears it. */
 MOE_API moe_status moe_timeout_site_read(void* ws, void* stream, int32_t* site);
 

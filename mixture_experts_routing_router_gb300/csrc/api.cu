@@ -37,9 +37,10 @@ void set_error(const char* fmt, ...) {
 
 void clear_error() { g_last_error[0] = 0; }
 
+bool aligned(const void* p, uintptr_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
 namespace {
 
-bool aligned(const void* p, uintptr_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool aligned_or_null(const void* p, uintptr_t a) { return p == nullptr || aligned(p, a); }
 
 moe_status check_shape(const moe_shape* s) {
@@ -62,6 +63,8 @@ moe_status check_shape(const moe_shape* s) {
     return MOE_OK;
 }
 
+}  // namespace
+
 moe_status check_ws(const moe_shape* s, const void* ws, size_t ws_bytes, bool whole_layer) {
     if (!aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
     const WsLayout L = ws_layout(*s);
@@ -69,14 +72,16 @@ moe_status check_ws(const moe_shape* s, const void* ws, size_t ws_bytes, bool wh
     return MOE_OK;
 }
 
-template <typename T>
-T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
-
 moe_status from_cuda(cudaError_t e) {
     if (e == cudaSuccess) return MOE_OK;
     if (g_last_error[0] == 0) set_error("%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
     return MOE_ERR_CUDA;
 }
+
+namespace {
+
+template <typename T>
+T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
 
 int up_rows(const moe_shape& s, int inter) { return (s.act == MOE_ACT_SWIGLU ? 2 : 1) * inter; }
 

@@ -5,7 +5,8 @@
 // routing/reduction"):
 //   out[t] = bf16( sum_{j<k} w[t,j] * y_perm[dest[t*k+j]] + y_shared[t] + residual[t] )
 // accumulated in FP32, j = 0..k-1 in order, then the shared-expert term, then
-// the residual (both optional).
+// the residual (both optional).  Without weights (w == NULL) the pairs are summed
+// as they are: the dispatch's gradient, dx[t] = sum_j dx_perm[dest[t*k+j]] + add[t].
 // One block per token row; 16-byte vectors (8 BF16) per thread; the k source
 // rows of a chunk are loaded together before they are summed in order.
 #include "common.cuh"
@@ -41,7 +42,7 @@ combine_kernel(int T, int HV, int k, const uint4* __restrict__ y_perm, const int
             const long long p = (long long)t * k + tid;
             const int d = __ldcg(dest + p);
             dsh[tid] = (d >= 0 && d < R) ? d : -1;
-            wsh[tid] = __ldcg(w + p);
+            wsh[tid] = w ? __ldcg(w + p) : 1.0f;
         }
     };
     // Inside moe_layer (gate set) the capacity verdict, dest and w come from

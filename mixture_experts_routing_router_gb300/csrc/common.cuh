@@ -86,7 +86,7 @@ constexpr unsigned long long kEarlyWaitNs = 200000ull;       // 200 us
 // Where a bounded wait gave up (WsHeader::timeout_site).
 enum TimeoutSite : int {
     kSiteNone = 0, kSiteLookback = 1, kSiteGemmProducer = 2, kSiteGemmMma = 3, kSiteGemmEpilogue = 4,
-    kSiteGemmDecode = 5, kSiteDecodeFfn = 6,
+    kSiteGemmDecode = 5, kSiteDecodeFfn = 6, kSiteGradProducer = 7, kSiteGradMma = 8, kSiteGradEpilogue = 9,
 };
 
 // ---------------------------------------------------------------------------
@@ -449,6 +449,7 @@ moe_status launch_decode_ffn(const moe_shape& s, const uint16_t* x_perm, const i
                              const uint16_t* w13, const uint16_t* w2, uint16_t* h, uint16_t* y_perm,
                              const int32_t* dest, const float* topk_w, const uint16_t* residual, uint16_t* out,
                              unsigned* sync, WsHeader* hdr, cudaStream_t st);
+// w: NULL takes unit weights (the dispatch's gradient).
 // gate: NULL, or (inside moe_layer) the workspace header whose capacity verdict,
 // when set, makes the kernel leave `out` untouched; the kernel also puts the
 // header's route_ready back to 0 for the next layer call.
@@ -553,10 +554,78 @@ bool make_tensor_map_glu_chunks(CUtensorMap* m, const void* base, long long rows
 bool make_tensor_map_u8_rows(CUtensorMap* m, const void* base, long long rows, long long cols, long long stride,
                              unsigned box_cols, unsigned box_rows);
 
+// Tensor map of [groups, rows, cols] BF16 (cols a multiple of 8), 128-byte
+// swizzle, boxes of 64 columns x box_rows rows of one group; rows past a
+// group's end read zeros, not the next group.
+bool make_tensor_map_bf16_groups(CUtensorMap* m, const void* base, long long groups, long long rows, long long cols,
+                                 unsigned box_rows);
+
+// ---- training: layer norm, gradients --------------------------------------------
+struct LayerNormProblem {
+    long long rows;
+    int hidden;
+    int type, wtype;                 // moe_type of x / y / dy / dx / dres, of gamma / beta
+    const void* x;
+    const void* gamma;
+    const void* beta;
+    float eps;
+    void* y;
+    float* mean;
+    float* rstd;
+    // backward
+    const void* dy;
+    const void* dres;
+    void* dx;
+    float* dgamma;
+    float* dbeta;
+    float* scratch;                  // [layernorm_parts(rows)][2][hidden]
+};
+// Partial sums of the weight's gradient: at most two blocks per SM of a GB300.
+constexpr int kLayerNormParts = 304;
+inline int layernorm_parts(long long rows) { return rows < kLayerNormParts ? (rows < 1 ? 1 : (int)rows) : kLayerNormParts; }
+cudaError_t launch_layernorm(const LayerNormProblem& p, cudaStream_t st);
+cudaError_t launch_layernorm_backward(const LayerNormProblem& p, cudaStream_t st);
+
+cudaError_t launch_combine_grad(const moe_shape& s, const uint16_t* dout, const uint16_t* y_perm, const int32_t* dest,
+                                const float* w, uint16_t* dy_perm, float* dw, cudaStream_t st);
+// Softmax routing with `w` (logits NULL), or sigmoid routing with `logits` and the route scale.
+cudaError_t launch_route_grad(const moe_shape& s, const float* logits, const int32_t* ids, const float* w, float scale,
+                              const float* dw, float* dlogits, WsHeader* hdr, cudaStream_t st);
+// h = act(pre) on the rows below offsets[experts].
+cudaError_t launch_act(const moe_shape& s, const int32_t* offsets, const uint16_t* pre, uint16_t* h, cudaStream_t st);
+
+// C[r, n] = sum_k a[r, k] w[g][k, n] for the rows r of group g, stored as BF16
+// with row stride ldo; with `pre` (same row stride) C becomes the gradient of
+// the activation's input: SwiGLU writes the gate half at n and the up half at
+// N + n, ReLU^2 one column.
+struct RowsGradProblem {
+    const uint16_t* a; long long rows; int K;
+    const uint16_t* w; int groups; int N;
+    const int32_t* offsets;
+    uint16_t* out; long long ldo;
+    const uint16_t* pre; int act;
+};
+moe_status launch_rows_grad(const RowsGradProblem& p, WsHeader* hdr, cudaStream_t st);
+// C[g][m, n] = sum over the rows r of group g of a[r, m] b[r, n]; wmode is a moe_wgrad value.
+struct WeightsGradProblem {
+    const uint16_t* a; int M;
+    const uint16_t* b; int N;
+    long long rows; int groups;
+    const int32_t* offsets;
+    void* out; int wmode;
+};
+moe_status launch_weights_grad(const WeightsGradProblem& p, WsHeader* hdr, cudaStream_t st);
+
 int device_sm_count();
 
 // The host-side shape checks every entry point applies (MOE_OK when valid).
 moe_status validate_shape(const moe_shape* s);
+
+// Shared by the entry points (api.cu, api_train.cu): 16- / 256-byte alignment of
+// a non-null pointer, the workspace's address and size, a CUDA call's status.
+bool aligned(const void* p, uintptr_t a);
+moe_status check_ws(const moe_shape* s, const void* ws, size_t ws_bytes, bool whole_layer);
+moe_status from_cuda(cudaError_t e);
 
 // Record a host-side failure description for moe_last_error_message (this thread).
 void set_error(const char* fmt, ...);

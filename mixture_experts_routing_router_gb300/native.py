@@ -29,13 +29,23 @@ MOE_ERR_INTERNAL = 8
 MOE_ACT_SWIGLU = 0
 MOE_ACT_RELU2 = 1
 
+MOE_TYPE_BF16 = 0
+MOE_TYPE_F32 = 1
+
+MOE_WGRAD_BF16 = 0
+MOE_WGRAD_F32 = 1
+MOE_WGRAD_F32_ADD = 2
+
 # every symbol include/moe.h declares
 EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_dispatch", "moe_expert_up",
            "moe_expert_down", "moe_expert_ffn", "moe_combine", "moe_layer", "moe_status_read",
            "moe_status_string", "moe_last_error_message", "moe_dispatch_noalloc", "moe_gate",
            "moe_route_sigmoid", "moe_expert_up_fp8", "moe_expert_down_fp8", "moe_layer_fp8",
            "moe_expert_up_nvfp4", "moe_expert_down_nvfp4", "moe_layer_nvfp4", "moe_workspace_set_wait",
-           "moe_timeout_site_read", "moe_ep_plan")
+           "moe_timeout_site_read", "moe_ep_plan", "moe_layernorm", "moe_layernorm_scratch_size",
+           "moe_layernorm_backward", "moe_combine_backward", "moe_dispatch_backward", "moe_route_backward",
+           "moe_route_sigmoid_backward", "moe_expert_up_train", "moe_expert_down_backward",
+           "moe_expert_up_backward")
 
 
 class MoEError(RuntimeError):
@@ -77,6 +87,7 @@ def lib():
             L = ctypes.CDLL(LIB_PATH)
             P, S = ctypes.c_void_p, ctypes.c_size_t
             SP = ctypes.POINTER(moe_shape)
+            I32, I64 = ctypes.c_int32, ctypes.c_int64
             sig = {
                 "moe_workspace_size": [SP, ctypes.POINTER(ctypes.c_size_t)],
                 "moe_workspace_init": [P, S, P],
@@ -100,6 +111,16 @@ def lib():
                 "moe_workspace_set_wait": [P, S, ctypes.c_uint64, ctypes.c_int32, P],
                 "moe_timeout_site_read": [P, P, ctypes.POINTER(ctypes.c_int32)],
                 "moe_ep_plan": [ctypes.c_int32] * 4 + [P] * 6,
+                "moe_layernorm": [I64, I32, I32, I32, P, P, P, ctypes.c_float, P, P, P, P],
+                "moe_layernorm_scratch_size": [I64, I32, ctypes.POINTER(ctypes.c_size_t)],
+                "moe_layernorm_backward": [I64, I32, I32, I32] + [P] * 10 + [S, P],
+                "moe_combine_backward": [SP, P, P, P, P, P, P, P, S, P],
+                "moe_dispatch_backward": [SP, P, P, P, P, P, S, P],
+                "moe_route_backward": [SP, P, P, P, P, P, S, P],
+                "moe_route_sigmoid_backward": [SP, P, P, ctypes.c_float, P, P, P, S, P],
+                "moe_expert_up_train": [SP, P, P, P, P, P, P, S, P],
+                "moe_expert_down_backward": [SP, P, P, P, P, P, P, P, I32, P, S, P],
+                "moe_expert_up_backward": [SP, P, P, P, P, P, P, I32, P, S, P],
             }
             for name, args in sig.items():
                 fn = getattr(L, name)
@@ -289,6 +310,117 @@ def moe_timeout_site_read(ws, stream=None) -> int:
     site = ctypes.c_int32(0)
     _check(lib().moe_timeout_site_read(_ptr(ws), _stream(stream), ctypes.byref(site)), "moe_timeout_site_read")
     return site.value
+
+
+# ---- training ---------------------------------------------------------------
+def _type(t):
+    try:
+        return {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}[t.dtype]
+    except KeyError:
+        raise ValueError(f"bfloat16 or float32 tensor expected, got {t.dtype}") from None
+
+
+def _norm_shape(x, gamma, *others):
+    """(rows, hidden) of a layer norm over x's last dimension; the other tensors match it."""
+    hidden = gamma.numel()
+    if gamma.dim() != 1 or x.dim() < 1 or x.shape[-1] != hidden:
+        raise ValueError(f"layer norm: weight of {tuple(gamma.shape)} for an input of {tuple(x.shape)}")
+    for t in others:
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+            raise ValueError(f"layer norm: {tuple(t.shape)} {t.dtype} beside an input of {tuple(x.shape)} {x.dtype}")
+    return x.numel() // hidden, hidden
+
+
+def _stat(t, n, what):
+    if t is not None and (t.dtype != torch.float32 or t.numel() != n):
+        raise ValueError(f"layer norm: {what} must be float32 with {n} elements, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def moe_layernorm(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
+    """Layer norm over x's last dimension into y (and the rows' mean and rstd)."""
+    rows, hidden = _norm_shape(x, gamma, y)
+    if beta.shape != gamma.shape or beta.dtype != gamma.dtype:
+        raise ValueError("layer norm: gamma and beta differ in shape or type")
+    _check(lib().moe_layernorm(rows, hidden, _type(x), _type(gamma), _ptr(x), _ptr(gamma), _ptr(beta), float(eps),
+                               _ptr(y), _ptr(_stat(mean, rows, "mean")), _ptr(_stat(rstd, rows, "rstd")),
+                               _stream(stream)), "moe_layernorm")
+
+
+def moe_layernorm_scratch_size(rows: int, hidden: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_layernorm_scratch_size(int(rows), int(hidden), ctypes.byref(n)), "moe_layernorm_scratch_size")
+    return n.value
+
+
+def layernorm_scratch(rows: int, hidden: int, device="cuda") -> torch.Tensor:
+    """The scratch moe_layernorm_backward needs for this many rows."""
+    return torch.empty(moe_layernorm_scratch_size(rows, hidden), dtype=torch.uint8, device=device)
+
+
+def moe_layernorm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, scratch, dres=None, stream=None):
+    """Gradient of moe_layernorm: dx (plus dres, the residual branch's gradient), dgamma, dbeta."""
+    rows, hidden = _norm_shape(x, gamma, dy, dx, dres)
+    _check(lib().moe_layernorm_backward(rows, hidden, _type(x), _type(gamma), _ptr(dy), _ptr(x), _ptr(gamma),
+                                        _ptr(_stat(mean, rows, "mean")), _ptr(_stat(rstd, rows, "rstd")), _ptr(dres),
+                                        _ptr(dx), _ptr(_stat(dgamma, hidden, "dgamma")),
+                                        _ptr(_stat(dbeta, hidden, "dbeta")), _ptr(scratch), _wsb(scratch),
+                                        _stream(stream)), "moe_layernorm_backward")
+
+
+def moe_combine_backward(shape, dout, y_perm, dest, topk_w, dy_perm, dtopk_w, ws, stream=None):
+    """Gradient of moe_combine: dy_perm, and dtopk_w unless it is None."""
+    _check(lib().moe_combine_backward(ctypes.byref(shape), _ptr(dout), _ptr(y_perm), _ptr(dest), _ptr(topk_w),
+                                      _ptr(dy_perm), _ptr(dtopk_w), _ptr(ws), _wsb(ws), _stream(stream)),
+           "moe_combine_backward")
+
+
+def moe_dispatch_backward(shape, dx_perm, dest, dx, ws, stream=None, add=None):
+    """Gradient of moe_dispatch's row copy, plus `add`."""
+    _check(lib().moe_dispatch_backward(ctypes.byref(shape), _ptr(dx_perm), _ptr(dest), _ptr(add), _ptr(dx), _ptr(ws),
+                                       _wsb(ws), _stream(stream)), "moe_dispatch_backward")
+
+
+def moe_route_backward(shape, topk_ids, topk_w, dtopk_w, dlogits, ws, stream=None):
+    _check(lib().moe_route_backward(ctypes.byref(shape), _ptr(topk_ids), _ptr(topk_w), _ptr(dtopk_w), _ptr(dlogits),
+                                    _ptr(ws), _wsb(ws), _stream(stream)), "moe_route_backward")
+
+
+def moe_route_sigmoid_backward(shape, logits, topk_ids, route_scale, dtopk_w, dlogits, ws, stream=None):
+    _check(lib().moe_route_sigmoid_backward(ctypes.byref(shape), _ptr(logits), _ptr(topk_ids), float(route_scale),
+                                            _ptr(dtopk_w), _ptr(dlogits), _ptr(ws), _wsb(ws), _stream(stream)),
+           "moe_route_sigmoid_backward")
+
+
+def moe_expert_up_train(shape, x_perm, offsets, w13, pre, h, ws, stream=None):
+    """Up projection that also keeps its pre-activations for the backward pass."""
+    _check(lib().moe_expert_up_train(ctypes.byref(shape), _ptr(x_perm), _ptr(offsets), _ptr(w13), _ptr(pre), _ptr(h),
+                                     _ptr(ws), _wsb(ws), _stream(stream)), "moe_expert_up_train")
+
+
+def _wgrad(dw, add):
+    """The moe_wgrad value of a weight gradient's tensor."""
+    if dw is None:
+        return MOE_WGRAD_BF16
+    if _type(dw) == MOE_TYPE_F32:
+        return MOE_WGRAD_F32_ADD if add else MOE_WGRAD_F32
+    if add:
+        raise ValueError("weight gradients are accumulated in float32")
+    return MOE_WGRAD_BF16
+
+
+def moe_expert_down_backward(shape, dy_perm, offsets, w2, pre, h, dpre, dw2, ws, stream=None, add=False):
+    """dpre (None: skipped) and dw2 (None: skipped; bfloat16 or float32, `add` accumulates into float32)."""
+    _check(lib().moe_expert_down_backward(ctypes.byref(shape), _ptr(dy_perm), _ptr(offsets), _ptr(w2), _ptr(pre),
+                                          _ptr(h), _ptr(dpre), _ptr(dw2), _wgrad(dw2, add), _ptr(ws), _wsb(ws),
+                                          _stream(stream)), "moe_expert_down_backward")
+
+
+def moe_expert_up_backward(shape, dpre, offsets, x_perm, w13, dx_perm, dw13, ws, stream=None, add=False):
+    """dx_perm (None: skipped) and dw13 (None: skipped; types as dw2)."""
+    _check(lib().moe_expert_up_backward(ctypes.byref(shape), _ptr(dpre), _ptr(offsets), _ptr(x_perm), _ptr(w13),
+                                        _ptr(dx_perm), _ptr(dw13), _wgrad(dw13, add), _ptr(ws), _wsb(ws),
+                                        _stream(stream)), "moe_expert_up_backward")
 
 
 def moe_ep_plan(experts: int, world: int, rank: int, capacity: int, counts_all):
