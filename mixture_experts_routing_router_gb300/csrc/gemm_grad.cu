@@ -19,8 +19,10 @@
 // rows also loads rows of the next group (or past the last one); each CTA's fixer
 // warp waits for that step's copies on a barrier of its own, zeroes the rows past
 // the bound up to the next multiple of 16 in both operands -- zeroing one would
-// leave 0 * NaN -- and then arrives on the leader's stage barrier; the MMA issues
-// only the 16-row slices that hold rows.  A group without rows writes zeros.
+// leave 0 * NaN --, the peer's fixer tells the leader's, and that arrives on the
+// stage barrier; the MMA issues only the 16-row slices that hold rows.  A group
+// without rows writes zeros.  (An arrival of the peer on the leader's barrier in
+// every step, released at cluster scope, took the step from 0.28 to 0.84 us.)
 //
 // Every wait is bounded; on a timeout the CTA stops issuing work, lets its copies
 // land, frees TMEM, raises MOE_ERR_TIMEOUT and returns.
@@ -39,8 +41,9 @@ constexpr int HALF = 128;                         // rows / columns each CTA con
 constexpr int OP_BYTES = HALF * BK * 2;           // 16 KiB an operand and CTA
 constexpr int BOX_BYTES = 64 * BK * 2;            // one 64 x 64 box of an MN-major operand
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
 constexpr int EPI_WARPS = 4;
+constexpr int EPI_BYTES = 8192;                   // staging of one epilogue warp
 constexpr int THREADS = 32 * (3 + EPI_WARPS);     // producer, MMA, epilogue, fixer
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int kBand = 8;                          // column tiles per band of the tile order
@@ -61,7 +64,7 @@ struct GParams {
 };
 
 struct Ctl {
-    unsigned long long full[STAGES], empty[STAGES], part[STAGES];
+    unsigned long long full[STAGES], empty[STAGES], part[STAGES], fixed[STAGES];
     unsigned long long tfull[2], tempty[2];
     unsigned long long drain;
     uint32_t tmem_base;
@@ -109,6 +112,12 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
         }
     }
 }
+// Arrive on a barrier of the pair without releasing earlier memory accesses at
+// cluster scope: it hands back an accumulator, and the stores of the tile before
+// need not be waited for.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, uint32_t bar_cluster, int x, int y,
                                                  int z) {
     asm volatile(
@@ -124,12 +133,188 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// max(z, 0) that keeps a NaN.
+__device__ __forceinline__ float relu(float z) { return z <= 0.f ? 0.f : z; }
 // d silu(g) u: dg = dh u s (1 + g (1 - s)), du = dh g s, s = sigmoid(g).
 __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& dg, float& du) {
-    const float s = 1.0f / (1.0f + __expf(-g));
+    const float s = __fdividef(1.0f, 1.0f + __expf(-g));
     const float gs = g * s;
     dg = dh * u * fmaf(gs, 1.0f - s, s);
     du = dh * gs;
+}
+
+// ---- epilogue -------------------------------------------------------------------
+// A warp turns 32 accumulator rows into output rows through its staging slot, so
+// that global memory is written in whole 64- or 128-byte row pieces: a thread holds
+// one row of the accumulator, and storing from there put 32 rows into each store
+// instruction (4.5 us a tile where the bytes take 1.5).  The 16-byte units of a
+// staged row are XORed with its index, so that both the row-wise and the
+// column-wise side are free of bank conflicts.
+__device__ __forceinline__ uint4* unit128(uint8_t* slot, int row, int u) {     // 128-byte rows
+    return reinterpret_cast<uint4*>(slot + row * 128 + ((u ^ (row & 7)) * 16));
+}
+__device__ __forceinline__ uint4* unit64(uint8_t* slot, int row, int u) {      // 64-byte rows
+    return reinterpret_cast<uint4*>(slot + row * 64 + ((u ^ ((row >> 1) & 3)) * 16));
+}
+__device__ __forceinline__ uint4 pack8(const uint32_t* v) {
+    return make_uint4(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), pack2(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                      pack2(__uint_as_float(v[4]), __uint_as_float(v[5])), pack2(__uint_as_float(v[6]), __uint_as_float(v[7])));
+}
+
+// BF16 output, 64 columns at a time.
+template <typename F>
+__device__ __forceinline__ void bf16_tile(uint32_t tl, bool empty, int rows, int n0, int N, __nv_bfloat16* out,
+                                          long long ldo, uint8_t* slot, int lane, F&& release) {
+#pragma unroll 1
+    for (int c = 0; c < TN / 64; ++c) {
+        uint8_t* s = slot + (c & 1) * 4096;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t v[32];
+            if (!empty) {
+                tmem_ld_32cols(tl + c * 64 + h * 32, v);
+                tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) *unit128(s, lane, h * 4 + u) = pack8(v + 8 * u);
+        }
+        if (c == TN / 64 - 1 && !empty) release();
+        __syncwarp();
+        const int u = lane & 7, col = n0 + c * 64 + u * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            if (r < rows && col < N) *reinterpret_cast<uint4*>(out + r * ldo + col) = *unit128(s, r, u);
+        }
+    }
+    __syncwarp();
+}
+
+// FP32 output (stored or added to), 32 columns at a time.
+template <typename F>
+__device__ __forceinline__ void f32_tile(const GParams& p, uint32_t tl, bool empty, int rows, int n0, float* out,
+                                         uint8_t* slot, int lane, F&& release) {
+#pragma unroll 1
+    for (int c = 0; c < TN / 32; ++c) {
+        uint8_t* s = slot + (c & 1) * 4096;
+        uint32_t v[32];
+        if (!empty) {
+            tmem_ld_32cols(tl + c * 32, v);
+            tmem_ld_wait();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) *unit128(s, lane, u) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+        if (c == TN / 32 - 1 && !empty) release();
+        __syncwarp();
+        const int u = lane & 7, col = n0 + c * 32 + u * 4;
+        const bool add = p.wmode == MOE_WGRAD_F32_ADD;
+        float4 old[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            old[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (add && r < rows && col < p.N) old[i] = *reinterpret_cast<const float4*>(out + r * p.ldo + col);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            const uint4 w = *unit128(s, r, u);
+            if (r < rows && col < p.N)
+                *reinterpret_cast<float4*>(out + r * p.ldo + col) =
+                    make_float4(old[i].x + __uint_as_float(w.x), old[i].y + __uint_as_float(w.y),
+                                old[i].z + __uint_as_float(w.z), old[i].w + __uint_as_float(w.w));
+        }
+    }
+    __syncwarp();
+}
+
+// The activation's gradient, 32 columns at a time: the pre-activations of a chunk
+// come into the slot with cp.async while the chunk before is worked on (two slots
+// of [gate 2 KiB | up 2 KiB]), each thread replaces its row's values by their
+// gradients, and the slot is written out.
+template <bool GLU>
+__device__ __forceinline__ void act_fetch(const GParams& p, int c, int m0, int rows, int row0, int n0, uint8_t* slot,
+                                          int lane) {
+    uint8_t* s = slot + (c & 1) * 4096;
+    const int u = lane & 3, col = n0 + c * 32 + u * 8;
+    if (c < TN / 32 && col < p.N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2);
+            if (r < rows) {
+                const __nv_bfloat16* src = p.pre + (size_t)(row0 + m0 + r) * p.ldp + col;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(unit64(s, r, u))), "l"(src) : "memory");
+                if (GLU)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                 :: "r"(smem_u32(unit64(s + 2048, r, u))), "l"(src + p.up_off) : "memory");
+            }
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <bool GLU>
+__device__ __forceinline__ void act_prefetch(const GParams& p, int m0, int rows, int row0, int n0, uint8_t* slot, int lane) {
+    act_fetch<GLU>(p, 0, m0, rows, row0, n0, slot, lane);
+    act_fetch<GLU>(p, 1, m0, rows, row0, n0, slot, lane);
+}
+template <bool GLU, typename F>
+__device__ __forceinline__ void act_tile(const GParams& p, uint32_t tl, int m0, int rows, int row0, int n0,
+                                         uint8_t* slot, int lane, F&& release) {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (size_t)(row0 + m0) * p.ldo;
+#pragma unroll 1
+    for (int c = 0; c < TN / 32; ++c) {
+        uint8_t* s = slot + (c & 1) * 4096;
+        uint32_t v[32];
+        tmem_ld_32cols(tl + c * 32, v);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        tmem_ld_wait();
+        if (c == TN / 32 - 1) release();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint4 g4 = *unit64(s, lane, u);
+            const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
+            uint32_t o[4];
+            if (GLU) {
+                const uint4 u4 = *unit64(s + 2048, lane, u);
+                const uint32_t uw[4] = {u4.x, u4.y, u4.z, u4.w};
+                uint32_t ou[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float dg0, du0, dg1, du1;
+                    swiglu_grad(__uint_as_float(v[8 * u + 2 * i]), bf_lo(gw[i]), bf_lo(uw[i]), dg0, du0);
+                    swiglu_grad(__uint_as_float(v[8 * u + 2 * i + 1]), bf_hi(gw[i]), bf_hi(uw[i]), dg1, du1);
+                    o[i] = pack2(dg0, dg1);
+                    ou[i] = pack2(du0, du1);
+                }
+                *unit64(s + 2048, lane, u) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[i] = pack2(__uint_as_float(v[8 * u + 2 * i]) * (2.0f * relu(bf_lo(gw[i]))),
+                                 __uint_as_float(v[8 * u + 2 * i + 1]) * (2.0f * relu(bf_hi(gw[i]))));
+            }
+            *unit64(s, lane, u) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        __syncwarp();
+        const int u = lane & 3, col = n0 + c * 32 + u * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2);
+            if (r < rows && col < p.N) {
+                *reinterpret_cast<uint4*>(out + r * p.ldo + col) = *unit64(s, r, u);
+                if (GLU) *reinterpret_cast<uint4*>(out + r * p.ldo + p.up_off + col) = *unit64(s + 2048, r, u);
+            }
+        }
+        __syncwarp();
+        act_fetch<GLU>(p, c + 2, m0, rows, row0, n0, slot, lane);
+    }
 }
 
 struct Tile { int g, mt, nt, row0, mrows; };
@@ -171,7 +356,8 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
-    Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * STAGE_BYTES);
+    uint8_t* epi_smem = smem + STAGES * STAGE_BYTES;
+    Ctl* ctl = reinterpret_cast<Ctl*>(epi_smem + EPI_WARPS * EPI_BYTES);
     int* prefix = reinterpret_cast<int*>(ctl + 1);
     int* rstart = prefix + (p.groups + 1);
     int* rcount = rstart + p.groups;
@@ -184,10 +370,10 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
 
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            // weights form: one arrival from each CTA (its producer, or its fixer)
-            mbar_init(smem_u32(&ctl->full[s]), kW ? 2 : 1);
+            mbar_init(smem_u32(&ctl->full[s]), 1);
             mbar_init(smem_u32(&ctl->empty[s]), 1);
             mbar_init(smem_u32(&ctl->part[s]), 1);
+            mbar_init(smem_u32(&ctl->fixed[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&ctl->tfull[a]), 1);
@@ -282,7 +468,6 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                             tma_load_2d(sb + BOX_BYTES, &tmB, part, b0 + 64, y);
                         } else {
                             if (rank == 0) mbar_arrive_expect_tx(full_local, 2 * STAGE_BYTES);
-                            else mbar_arrive_cluster(full_leader);
                             tma_load_2d_pair(sa, &tmA, full_leader, a0, y);
                             tma_load_2d_pair(sa + BOX_BYTES, &tmA, full_leader, a0 + 64, y);
                             tma_load_2d_pair(sb, &tmB, full_leader, b0, y);
@@ -325,7 +510,9 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 const uint32_t d = tmem_base + (uint32_t)(acc * TN);
                 for (int i = 0; i < nk; ++i) {
                     const uint32_t full = smem_u32(&ctl->full[stage]);
-                    if (!(kW ? mbar_wait_cluster(full, ph, abort) : mbar_wait_bounded(full, ph, abort))) {
+                    const int left = kW ? t.mrows - i * BK : BK;
+                    // a partial step: the other CTA's fixer wrote its shared memory
+                    if (!(kW && left < BK ? mbar_wait_cluster(full, ph, abort) : mbar_wait_bounded(full, ph, abort))) {
                         ok = false;
                         break;
                     }
@@ -333,7 +520,6 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                     const uint32_t sa = smem_base + stage * STAGE_BYTES;
                     const uint64_t ad = kW ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
                     const uint64_t bd = sdesc_mn_sw128(sa + OP_BYTES);
-                    const int left = kW ? t.mrows - i * BK : BK;
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
                         if (!kW || kk * 16 < left)
@@ -357,16 +543,19 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             }
         }
     } else if (warp < 2 + EPI_WARPS) {
-        // ---------------- epilogue (both CTAs): thread = one row of the tile ----------------
+        // ---------------- epilogue (both CTAs): a warp = 32 rows of the tile ----------------
         const int q = warp & 3;
+        uint8_t* epi = epi_smem + q * EPI_BYTES;
         int acc = 0;
         uint32_t aph = 0;
         for (int tile = pair; tile < total; tile += npairs) {
             const Tile t = decode_tile<KIND>(tile, prefix, rstart, rcount, p.groups, ntm, ntn);
-            const int m = t.mt * TM + (int)rank * HALF + q * 32 + lane;
-            const bool row_ok = m < (kW ? p.M : t.mrows);
+            const int m0 = t.mt * TM + (int)rank * HALF + q * 32;      // this warp's 32 rows
+            const int rows = (kW ? p.M : t.mrows) - m0;                // of which below the bound
             const int n0 = t.nt * TN;
             const bool empty = kW && t.mrows == 0;
+            if (KIND == kRowsSwiGLU || KIND == kRowsReLU2)
+                act_prefetch<KIND == kRowsSwiGLU>(p, m0, rows, t.row0, n0, epi, lane);
             if (!empty) {
                 if (!mbar_wait_bounded(smem_u32(&ctl->tfull[acc]), aph, abort)) {
                     if (lane == 0) {
@@ -378,85 +567,31 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 tc_fence_after();
             }
             const uint32_t tl = tmem_base + (uint32_t)(acc * TN) + ((uint32_t)(q * 32) << 16);
-            const size_t orow = kW ? ((size_t)t.g * p.M + m) * p.ldo : (size_t)(t.row0 + m) * p.ldo;
-#pragma unroll 1
-            for (int c = 0; c < TN / 32; ++c) {
-                const int col0 = n0 + c * 32;
-                uint32_t v[32];
-                if (!empty) {
-                    tmem_ld_32cols(tl + c * 32, v);
-                    tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0u;
-                }
-                if (!row_ok || (empty && p.wmode == MOE_WGRAD_F32_ADD)) continue;
-                if (kW && p.wmode != MOE_WGRAD_BF16) {
-                    float* o = reinterpret_cast<float*>(p.out) + orow;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (col0 + 4 * i >= p.N) break;
-                        float4* o4 = reinterpret_cast<float4*>(o + col0 + 4 * i);
-                        float4 f = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                               __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
-                        if (p.wmode == MOE_WGRAD_F32_ADD) {
-                            const float4 old = *o4;
-                            f.x += old.x; f.y += old.y; f.z += old.z; f.w += old.w;
-                        }
-                        *o4 = f;
-                    }
-                    continue;
-                }
-                __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + orow;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int col = col0 + 8 * b;
-                    if (col >= p.N) break;
-                    float f[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * b + i]);
-                    if (KIND == kRowsSwiGLU) {
-                        const __nv_bfloat16* pr = p.pre + (size_t)(t.row0 + m) * p.ldp;
-                        const uint4 g4 = *reinterpret_cast<const uint4*>(pr + col);
-                        const uint4 u4 = *reinterpret_cast<const uint4*>(pr + p.up_off + col);
-                        const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
-                        uint32_t og[4], ou[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float dg0, du0, dg1, du1;
-                            swiglu_grad(f[2 * i], bf_lo(gw[i]), bf_lo(uw[i]), dg0, du0);
-                            swiglu_grad(f[2 * i + 1], bf_hi(gw[i]), bf_hi(uw[i]), dg1, du1);
-                            og[i] = pack2(dg0, dg1);
-                            ou[i] = pack2(du0, du1);
-                        }
-                        *reinterpret_cast<uint4*>(o + col) = make_uint4(og[0], og[1], og[2], og[3]);
-                        *reinterpret_cast<uint4*>(o + p.up_off + col) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-                        continue;
-                    }
-                    if (KIND == kRowsReLU2) {
-                        const uint4 z4 = *reinterpret_cast<const uint4*>(p.pre + (size_t)(t.row0 + m) * p.ldp + col);
-                        const uint32_t zw[4] = {z4.x, z4.y, z4.z, z4.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            f[2 * i] *= 2.0f * fmaxf(bf_lo(zw[i]), 0.f);
-                            f[2 * i + 1] *= 2.0f * fmaxf(bf_hi(zw[i]), 0.f);
-                        }
-                    }
-                    *reinterpret_cast<uint4*>(o + col) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]),
-                                                                    pack2(f[4], f[5]), pack2(f[6], f[7]));
-                }
+            auto release = [&] {               // the accumulator is read: the next tile may overwrite it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&ctl->tempty[acc]), 0));
+            };
+            if (KIND == kRowsSwiGLU || KIND == kRowsReLU2) {
+                act_tile<KIND == kRowsSwiGLU>(p, tl, m0, rows, t.row0, n0, epi, lane, release);
+            } else if (kW && p.wmode != MOE_WGRAD_BF16) {
+                if (!(empty && p.wmode == MOE_WGRAD_F32_ADD))
+                    f32_tile(p, tl, empty, rows, n0, static_cast<float*>(p.out) + ((size_t)t.g * p.M + m0) * p.ldo, epi,
+                             lane, release);
+            } else {
+                const size_t row = kW ? (size_t)t.g * p.M + m0 : (size_t)(t.row0 + m0);
+                bf16_tile(tl, empty, rows, n0, p.N, static_cast<__nv_bfloat16*>(p.out) + row * p.ldo, p.ldo, epi, lane,
+                          release);
             }
             if (empty) continue;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->tempty[acc]), 0));
             acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else if (kW) {
         // ---------------- fixer (both CTAs): partial reduction steps ----------------
         int stage = 0;
-        uint32_t pph = 0;                          // parity of part[s] in bit s
+        uint32_t pph = 0;                          // parity of part[s] and fixed[s] in bit s
         bool ok = true;
         for (int tile = pair; tile < total && ok; tile += npairs) {
             const Tile t = decode_tile<KIND>(tile, prefix, rstart, rcount, p.groups, ntm, ntn);
@@ -464,8 +599,9 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const int rem = t.mrows & (BK - 1);
             if (rem) {
                 const int s = (stage + nk - 1) % STAGES;
-                if (!mbar_wait_bounded(smem_u32(&ctl->part[s]), (pph >> s) & 1u, abort)) { ok = false; break; }
+                const uint32_t parity = (pph >> s) & 1u;
                 pph ^= 1u << s;
+                if (!mbar_wait_bounded(smem_u32(&ctl->part[s]), parity, abort)) { ok = false; break; }
                 const int end = (rem + 15) & ~15;
                 // four boxes of 128-byte rows; the swizzle stays inside a row
                 for (int i = lane; i < 4 * (end - rem) * 8; i += 32) {
@@ -475,7 +611,12 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->full[s]), 0));
+                if (rank != 0) {
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->fixed[s]), 0));
+                } else {
+                    if (!mbar_wait_cluster(smem_u32(&ctl->fixed[s]), parity, abort)) { ok = false; break; }
+                    if (lane == 0) mbar_arrive_cluster(smem_u32(&ctl->full[s]));
+                }
             }
             stage = (stage + nk) % STAGES;
         }
@@ -496,7 +637,7 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
 }
 
 size_t smem_bytes(int groups) {
-    return 1024 + (size_t)STAGES * STAGE_BYTES + sizeof(Ctl) + 3 * (size_t)(groups + 1) * 4;
+    return 1024 + (size_t)STAGES * STAGE_BYTES + EPI_WARPS * EPI_BYTES + sizeof(Ctl) + 3 * (size_t)(groups + 1) * 4;
 }
 
 template <int KIND>
@@ -547,7 +688,7 @@ act_kernel(long long rows, int IV, long long ldv, const int32_t* __restrict__ of
             if (GLU) {
                 o[j] = pack2(x0 / (1.0f + __expf(-x0)) * bf_lo(uw[j]), x1 / (1.0f + __expf(-x1)) * bf_hi(uw[j]));
             } else {
-                const float z0 = fmaxf(x0, 0.f), z1 = fmaxf(x1, 0.f);
+                const float z0 = relu(x0), z1 = relu(x1);
                 o[j] = pack2(z0 * z0, z1 * z1);
             }
         }
