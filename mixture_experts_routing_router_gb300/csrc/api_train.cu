@@ -181,25 +181,15 @@ moe_status moe_expert_down_backward(const moe_shape* shape, const uint16_t* dy_p
     if (dpre && (!aligned(dpre, 16) || !aligned(w2, 16) || !aligned(pre, 16))) return MOE_ERR_INVALID_ARG;
     if (dw2 && (!aligned(dw2, 16) || !aligned(h, 16))) return MOE_ERR_INVALID_ARG;
     const moe_shape& s = *shape;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const long long R = (long long)s.tokens * s.top_k;
-    if (dpre) {
-        RowsGradProblem g{};
-        g.a = dy_perm; g.rows = R; g.K = s.hidden;
-        g.w = w2; g.groups = s.experts; g.N = s.inter;
-        g.offsets = offsets;
-        g.out = dpre; g.ldo = up_rows(s);
-        g.pre = pre; g.act = s.act;
-        if ((r = launch_rows_grad(g, header(ws), st)) != MOE_OK) return r;
-    }
-    if (!dw2) return MOE_OK;
-    WeightsGradProblem q{};
-    q.a = dy_perm; q.M = s.hidden;
-    q.b = h; q.N = s.inter;
-    q.rows = R; q.groups = s.experts;
-    q.offsets = offsets;
-    q.out = dw2; q.wmode = wgrad;
-    return launch_weights_grad(q, header(ws), st);
+    ExpertGradProblem g{};
+    g.a = dy_perm; g.rows = (long long)s.tokens * s.top_k;
+    g.offsets = offsets; g.groups = s.experts;
+    g.w = w2; g.K = s.hidden; g.N = s.inter;
+    g.out = dpre; g.ldo = up_rows(s);
+    g.pre = pre; g.act = s.act;
+    g.wb = h; g.wM = s.hidden; g.wN = s.inter;
+    g.wout = dw2; g.wmode = wgrad;
+    return launch_expert_grad(g, header(ws), static_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_expert_up_backward(const moe_shape* shape, const uint16_t* dpre, const int32_t* offsets,
@@ -212,24 +202,14 @@ moe_status moe_expert_up_backward(const moe_shape* shape, const uint16_t* dpre, 
     if (dx_perm && (!aligned(dx_perm, 16) || !aligned(w13, 16))) return MOE_ERR_INVALID_ARG;
     if (dw13 && (!aligned(dw13, 16) || !aligned(x_perm, 16))) return MOE_ERR_INVALID_ARG;
     const moe_shape& s = *shape;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const long long R = (long long)s.tokens * s.top_k;
-    if (dx_perm) {
-        RowsGradProblem g{};
-        g.a = dpre; g.rows = R; g.K = up_rows(s);
-        g.w = w13; g.groups = s.experts; g.N = s.hidden;
-        g.offsets = offsets;
-        g.out = dx_perm; g.ldo = s.hidden;
-        if ((r = launch_rows_grad(g, header(ws), st)) != MOE_OK) return r;
-    }
-    if (!dw13) return MOE_OK;
-    WeightsGradProblem q{};
-    q.a = dpre; q.M = up_rows(s);
-    q.b = x_perm; q.N = s.hidden;
-    q.rows = R; q.groups = s.experts;
-    q.offsets = offsets;
-    q.out = dw13; q.wmode = wgrad;
-    return launch_weights_grad(q, header(ws), st);
+    ExpertGradProblem g{};
+    g.a = dpre; g.rows = (long long)s.tokens * s.top_k;
+    g.offsets = offsets; g.groups = s.experts;
+    g.w = w13; g.K = up_rows(s); g.N = s.hidden;
+    g.out = dx_perm; g.ldo = s.hidden;
+    g.wb = x_perm; g.wM = up_rows(s); g.wN = s.hidden;
+    g.wout = dw13; g.wmode = wgrad;
+    return launch_expert_grad(g, header(ws), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -594,27 +594,23 @@ cudaError_t launch_route_grad(const moe_shape& s, const float* logits, const int
 // h = act(pre) on the rows below offsets[experts].
 cudaError_t launch_act(const moe_shape& s, const int32_t* offsets, const uint16_t* pre, uint16_t* h, cudaStream_t st);
 
-// C[r, n] = sum_k a[r, k] w[g][k, n] for the rows r of group g, stored as BF16
-// with row stride ldo; with `pre` (same row stride) C becomes the gradient of
-// the activation's input: SwiGLU writes the gate half at n and the up half at
-// N + n, ReLU^2 one column.
-struct RowsGradProblem {
-    const uint16_t* a; long long rows; int K;
-    const uint16_t* w; int groups; int N;
-    const int32_t* offsets;
+// The gradient GEMMs of one expert projection, either or both of:
+//   rows form (out):     C[r, n] = sum_k a[r, k] w[g][k, n] for the rows r of group g,
+//                        BF16 with row stride ldo; with `pre` (same row stride) C becomes
+//                        the gradient of the activation's input: SwiGLU writes the gate
+//                        half at n and the up half at N + n, ReLU^2 one column;
+//   weights form (wout): C[g][m, n] = sum over the rows r of group g of a[r, m] wb[r, n],
+//                        stored as the moe_wgrad value wmode says.
+struct ExpertGradProblem {
+    const uint16_t* a; long long rows;
+    const int32_t* offsets; int groups;
+    const uint16_t* w; int K, N;
     uint16_t* out; long long ldo;
     const uint16_t* pre; int act;
+    const uint16_t* wb; int wM, wN;      // wM == K: a's columns
+    void* wout; int wmode;
 };
-moe_status launch_rows_grad(const RowsGradProblem& p, WsHeader* hdr, cudaStream_t st);
-// C[g][m, n] = sum over the rows r of group g of a[r, m] b[r, n]; wmode is a moe_wgrad value.
-struct WeightsGradProblem {
-    const uint16_t* a; int M;
-    const uint16_t* b; int N;
-    long long rows; int groups;
-    const int32_t* offsets;
-    void* out; int wmode;
-};
-moe_status launch_weights_grad(const WeightsGradProblem& p, WsHeader* hdr, cudaStream_t st);
+moe_status launch_expert_grad(const ExpertGradProblem& p, WsHeader* hdr, cudaStream_t st);
 
 int device_sm_count();
 

@@ -10,10 +10,15 @@
 //
 // Both forms run on CTA pairs: a cluster of two CTAs owns a 256 x 256 output tile
 // through tcgen05.mma.cta_group::2, each CTA loading its 128 A rows (or columns)
-// and its 128 B columns per 64-deep step (32 KiB a stage, six stages) and holding
-// 128 rows of two 256-column accumulators, so the epilogue of one tile runs under
-// the next tile's main loop.  The rows form's epilogue applies the activation's
-// derivative: dpre = act'(pre) * dh, from the saved pre-activations.
+// and its 128 B columns per 64-deep step (32 KiB a stage, five or six stages) and
+// holding 128 rows of two 256-column accumulators, so the epilogue of one tile runs
+// under the next tile's main loop.  The rows form's epilogue applies the
+// activation's derivative: dpre = act'(pre) * dh, from the saved pre-activations.
+//
+// One launch does both forms of one projection (dh with dW2, dx with dW13): they
+// read the same rows and need nothing of each other, a launch less costs a small
+// layer 8 us less, and the short tiles of the weights form fill the last, partly
+// filled round of the long tiles of the rows form.
 //
 // The weights form reduces over a group's rows.  A last step of fewer than 64
 // rows also loads rows of the next group (or past the last one); each CTA's fixer
@@ -21,8 +26,7 @@
 // the bound up to the next multiple of 16 in both operands -- zeroing one would
 // leave 0 * NaN --, the peer's fixer tells the leader's, and that arrives on the
 // stage barrier; the MMA issues only the 16-row slices that hold rows.  A group
-// without rows writes zeros.  (An arrival of the peer on the leader's barrier in
-// every step, released at cluster scope, took the step from 0.28 to 0.84 us.)
+// without rows writes zeros.
 //
 // Every wait is bounded; on a timeout the CTA stops issuing work, lets its copies
 // land, frees TMEM, raises MOE_ERR_TIMEOUT and returns.
@@ -30,46 +34,50 @@
 
 #include <climits>
 #include <mutex>
+#include <type_traits>
 
 namespace moe {
 namespace {
 
-enum GradKind : int { kRowsSwiGLU = 0, kRowsReLU2 = 1, kRowsPlain = 2, kWeights = 3 };
+enum Act : int { kSwiGLU = 0, kReLU2 = 1, kPlain = 2 };      // what the rows form's epilogue applies
 
 constexpr int TM = 256, TN = 256, BK = 64;        // output tile of the pair, reduction step
 constexpr int HALF = 128;                         // rows / columns each CTA contributes
 constexpr int OP_BYTES = HALF * BK * 2;           // 16 KiB an operand and CTA
 constexpr int BOX_BYTES = 64 * BK * 2;            // one 64 x 64 box of an MN-major operand
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
-constexpr int STAGES = 5;
-constexpr int EPI_WARPS = 4;
-constexpr int EPI_BYTES = 8192;                   // staging of one epilogue warp
+constexpr int MAX_STAGES = 6;                     // five where the group tables leave no room for six
+constexpr int EPI_WARPS = 8;                      // two per 32 rows, 128 columns each
+constexpr int EPI_COLS = TN * 4 / EPI_WARPS;
+constexpr int EPI_BYTES = 4096;                   // staging of one epilogue warp
 constexpr int THREADS = 32 * (3 + EPI_WARPS);     // producer, MMA, epilogue, fixer
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int kBand = 8;                          // column tiles per band of the tile order
-constexpr int MAX_DYN_SMEM = 216 * 1024;
+constexpr int MAX_DYN_SMEM = 232448 - 1024;       // the opt-in limit less the kernel's static part
 
 struct GParams {
     const int32_t* offsets;
     int groups, a_rows;              // bucket bounds are clamped to [0, a_rows]
-    int K;                           // rows form: reduction length
-    int M, N;                        // weights form: output rows; output columns
-    void* out;
-    long long ldo;
-    const __nv_bfloat16* pre;        // activation forms: [a_rows, up] pre-activations
-    long long ldp;
-    int up_off;                      // SwiGLU: columns from gate to up half
-    int wmode;                       // weights form: moe_wgrad
+    int stages;                      // of the shared-memory ring
     WsHeader* hdr;
+    // rows form (N == 0: not asked for)
+    int K, N;
+    __nv_bfloat16* out;
+    long long ldo;
+    const __nv_bfloat16* pre;        // [a_rows, up] pre-activations, row stride ldo
+    int up_off;                      // SwiGLU: columns from gate to up half
+    // weights form (wM == 0: not asked for)
+    int wM, wN, wmode;               // wmode: moe_wgrad
+    void* wout;
 };
 
 struct Ctl {
-    unsigned long long full[STAGES], empty[STAGES], part[STAGES], fixed[STAGES];
+    unsigned long long full[MAX_STAGES], empty[MAX_STAGES], part[MAX_STAGES], fixed[MAX_STAGES];
     unsigned long long tfull[2], tempty[2];
     unsigned long long drain;
     uint32_t tmem_base;
     int abort;
-    int total_tiles;
+    int rows_tiles;
 };
 
 // Instruction descriptor bits: operand A / B is MN-major.
@@ -112,11 +120,16 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
         }
     }
 }
-// Arrive on a barrier of the pair without releasing earlier memory accesses at
-// cluster scope: it hands back an accumulator, and the stores of the tile before
-// need not be waited for.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+// Relaxed arrival on a barrier of the pair: it hands back an accumulator, whose
+// reads tcgen05.fence::before_thread_sync orders; a release would also wait for the
+// warp's stores of the tile before.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+}
+// Release, at cluster scope, of this CTA's shared memory only.  (A full release
+// waits for every store of the thread: it took the fixer 0.5 us and more a tile.)
+__device__ __forceinline__ void fence_release_smem_cluster() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
 }
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, uint32_t bar_cluster, int x, int y,
                                                  int z) {
@@ -153,8 +166,8 @@ __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& d
 __device__ __forceinline__ uint4* unit128(uint8_t* slot, int row, int u) {     // 128-byte rows
     return reinterpret_cast<uint4*>(slot + row * 128 + ((u ^ (row & 7)) * 16));
 }
-__device__ __forceinline__ uint4* unit64(uint8_t* slot, int row, int u) {      // 64-byte rows
-    return reinterpret_cast<uint4*>(slot + row * 64 + ((u ^ ((row >> 1) & 3)) * 16));
+__device__ __forceinline__ uint4* unit32(uint8_t* slot, int row, int u) {      // 32-byte rows
+    return reinterpret_cast<uint4*>(slot + row * 32 + ((u ^ ((row >> 2) & 1)) * 16));
 }
 __device__ __forceinline__ uint4 pack8(const uint32_t* v) {
     return make_uint4(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), pack2(__uint_as_float(v[2]), __uint_as_float(v[3])),
@@ -164,95 +177,95 @@ __device__ __forceinline__ uint4 pack8(const uint32_t* v) {
 // BF16 output, 64 columns at a time.
 template <typename F>
 __device__ __forceinline__ void bf16_tile(uint32_t tl, bool empty, int rows, int n0, int N, __nv_bfloat16* out,
-                                          long long ldo, uint8_t* slot, int lane, F&& release) {
+                                          long long ldo, uint8_t* s, int lane, F&& release) {
 #pragma unroll 1
-    for (int c = 0; c < TN / 64; ++c) {
-        uint8_t* s = slot + (c & 1) * 4096;
+    for (int c = 0; c < EPI_COLS / 64; ++c) {
+        uint32_t v[2][32];
+        if (!empty) {
+            tmem_ld_32cols(tl + c * 64, v[0]);
+            tmem_ld_32cols(tl + c * 64 + 32, v[1]);
+            tmem_ld_wait();
+            if (c == EPI_COLS / 64 - 1) release();
+        } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t v[32];
-            if (!empty) {
-                tmem_ld_32cols(tl + c * 64 + h * 32, v);
-                tmem_ld_wait();
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0u;
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) *unit128(s, lane, h * 4 + u) = pack8(v + 8 * u);
+            for (int i = 0; i < 32; ++i) v[0][i] = v[1][i] = 0u;
         }
-        if (c == TN / 64 - 1 && !empty) release();
+#pragma unroll
+        for (int u = 0; u < 8; ++u) *unit128(s, lane, u) = pack8(v[u >> 2] + 8 * (u & 3));
         __syncwarp();
         const int u = lane & 7, col = n0 + c * 64 + u * 8;
+        uint4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = *unit128(s, i * 4 + (lane >> 3), u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = i * 4 + (lane >> 3);
-            if (r < rows && col < N) *reinterpret_cast<uint4*>(out + r * ldo + col) = *unit128(s, r, u);
+            if (r < rows && col < N) *reinterpret_cast<uint4*>(out + r * ldo + col) = w[i];
         }
+        __syncwarp();
     }
-    __syncwarp();
 }
 
 // FP32 output (stored or added to), 32 columns at a time.
 template <typename F>
 __device__ __forceinline__ void f32_tile(const GParams& p, uint32_t tl, bool empty, int rows, int n0, float* out,
-                                         uint8_t* slot, int lane, F&& release) {
+                                         uint8_t* s, int lane, F&& release) {
+    const bool add = p.wmode == MOE_WGRAD_F32_ADD;
 #pragma unroll 1
-    for (int c = 0; c < TN / 32; ++c) {
-        uint8_t* s = slot + (c & 1) * 4096;
-        uint32_t v[32];
-        if (!empty) {
-            tmem_ld_32cols(tl + c * 32, v);
-            tmem_ld_wait();
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) *unit128(s, lane, u) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-        if (c == TN / 32 - 1 && !empty) release();
-        __syncwarp();
+    for (int c = 0; c < EPI_COLS / 32; ++c) {
         const int u = lane & 7, col = n0 + c * 32 + u * 4;
-        const bool add = p.wmode == MOE_WGRAD_F32_ADD;
         float4 old[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = i * 4 + (lane >> 3);
             old[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (add && r < rows && col < p.N) old[i] = *reinterpret_cast<const float4*>(out + r * p.ldo + col);
+            if (add && r < rows && col < p.wN) old[i] = *reinterpret_cast<const float4*>(out + (size_t)r * p.wN + col);
         }
+        uint32_t v[32];
+        if (!empty) {
+            tmem_ld_32cols(tl + c * 32, v);
+            tmem_ld_wait();
+            if (c == EPI_COLS / 32 - 1) release();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *unit128(s, lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = i * 4 + (lane >> 3);
             const uint4 w = *unit128(s, r, u);
-            if (r < rows && col < p.N)
-                *reinterpret_cast<float4*>(out + r * p.ldo + col) =
+            if (r < rows && col < p.wN)
+                *reinterpret_cast<float4*>(out + (size_t)r * p.wN + col) =
                     make_float4(old[i].x + __uint_as_float(w.x), old[i].y + __uint_as_float(w.y),
                                 old[i].z + __uint_as_float(w.z), old[i].w + __uint_as_float(w.w));
         }
+        __syncwarp();
     }
-    __syncwarp();
 }
 
-// The activation's gradient, 32 columns at a time: the pre-activations of a chunk
-// come into the slot with cp.async while the chunk before is worked on (two slots
-// of [gate 2 KiB | up 2 KiB]), each thread replaces its row's values by their
-// gradients, and the slot is written out.
+// The activation's gradient, 16 columns at a time: the pre-activations of a chunk
+// come into the slot with cp.async while the chunk before is worked on (two halves
+// of [gate 1 KiB | up 1 KiB]), each thread replaces its row's values by their
+// gradients, and the half is written out.
+constexpr int ACT_COLS = 16, ACT_CHUNKS = EPI_COLS / ACT_COLS;
 template <bool GLU>
 __device__ __forceinline__ void act_fetch(const GParams& p, int c, int m0, int rows, int row0, int n0, uint8_t* slot,
                                           int lane) {
-    uint8_t* s = slot + (c & 1) * 4096;
-    const int u = lane & 3, col = n0 + c * 32 + u * 8;
-    if (c < TN / 32 && col < p.N) {
+    uint8_t* s = slot + (c & 1) * 2048;
+    const int u = lane & 1, col = n0 + c * ACT_COLS + u * 8;
+    if (c < ACT_CHUNKS && col < p.N) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + (lane >> 2);
+        for (int i = 0; i < 2; ++i) {
+            const int r = i * 16 + (lane >> 1);
             if (r < rows) {
-                const __nv_bfloat16* src = p.pre + (size_t)(row0 + m0 + r) * p.ldp + col;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(unit64(s, r, u))), "l"(src) : "memory");
+                const __nv_bfloat16* src = p.pre + (size_t)(row0 + m0 + r) * p.ldo + col;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(unit32(s, r, u))), "l"(src) : "memory");
                 if (GLU)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                                 :: "r"(smem_u32(unit64(s + 2048, r, u))), "l"(src + p.up_off) : "memory");
+                                 :: "r"(smem_u32(unit32(s + 1024, r, u))), "l"(src + p.up_off) : "memory");
             }
         }
     }
@@ -262,27 +275,39 @@ template <bool GLU>
 __device__ __forceinline__ void act_prefetch(const GParams& p, int m0, int rows, int row0, int n0, uint8_t* slot, int lane) {
     act_fetch<GLU>(p, 0, m0, rows, row0, n0, slot, lane);
     act_fetch<GLU>(p, 1, m0, rows, row0, n0, slot, lane);
+    // the rest of the warp's rows into L2 (64 columns a line), while the tile is multiplied
+    if (lane < rows) {
+        const __nv_bfloat16* src = p.pre + (size_t)(row0 + m0 + lane) * p.ldo;
+#pragma unroll
+        for (int c = 0; c < EPI_COLS; c += 64) {
+            const int col = n0 + c;
+            if (col < p.N) {
+                asm volatile("prefetch.global.L2 [%0];" :: "l"(src + col));
+                if (GLU) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + p.up_off + col));
+            }
+        }
+    }
 }
 template <bool GLU, typename F>
 __device__ __forceinline__ void act_tile(const GParams& p, uint32_t tl, int m0, int rows, int row0, int n0,
                                          uint8_t* slot, int lane, F&& release) {
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (size_t)(row0 + m0) * p.ldo;
+    __nv_bfloat16* out = p.out + (size_t)(row0 + m0) * p.ldo;
 #pragma unroll 1
-    for (int c = 0; c < TN / 32; ++c) {
-        uint8_t* s = slot + (c & 1) * 4096;
-        uint32_t v[32];
-        tmem_ld_32cols(tl + c * 32, v);
+    for (int c = 0; c < ACT_CHUNKS; ++c) {
+        uint8_t* s = slot + (c & 1) * 2048;
+        uint32_t v[16];
+        tmem_ld_16cols(tl + c * ACT_COLS, v);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
         tmem_ld_wait();
-        if (c == TN / 32 - 1) release();
+        if (c == ACT_CHUNKS - 1) release();
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const uint4 g4 = *unit64(s, lane, u);
+        for (int u = 0; u < 2; ++u) {
+            const uint4 g4 = *unit32(s, lane, u);
             const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
             uint32_t o[4];
             if (GLU) {
-                const uint4 u4 = *unit64(s + 2048, lane, u);
+                const uint4 u4 = *unit32(s + 1024, lane, u);
                 const uint32_t uw[4] = {u4.x, u4.y, u4.z, u4.w};
                 uint32_t ou[4];
 #pragma unroll
@@ -293,23 +318,23 @@ __device__ __forceinline__ void act_tile(const GParams& p, uint32_t tl, int m0, 
                     o[i] = pack2(dg0, dg1);
                     ou[i] = pack2(du0, du1);
                 }
-                *unit64(s + 2048, lane, u) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+                *unit32(s + 1024, lane, u) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     o[i] = pack2(__uint_as_float(v[8 * u + 2 * i]) * (2.0f * relu(bf_lo(gw[i]))),
                                  __uint_as_float(v[8 * u + 2 * i + 1]) * (2.0f * relu(bf_hi(gw[i]))));
             }
-            *unit64(s, lane, u) = make_uint4(o[0], o[1], o[2], o[3]);
+            *unit32(s, lane, u) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         __syncwarp();
-        const int u = lane & 3, col = n0 + c * 32 + u * 8;
+        const int u = lane & 1, col = n0 + c * ACT_COLS + u * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + (lane >> 2);
+        for (int i = 0; i < 2; ++i) {
+            const int r = i * 16 + (lane >> 1);
             if (r < rows && col < p.N) {
-                *reinterpret_cast<uint4*>(out + r * p.ldo + col) = *unit64(s, r, u);
-                if (GLU) *reinterpret_cast<uint4*>(out + r * p.ldo + p.up_off + col) = *unit64(s + 2048, r, u);
+                *reinterpret_cast<uint4*>(out + r * p.ldo + col) = *unit32(s, r, u);
+                if (GLU) *reinterpret_cast<uint4*>(out + r * p.ldo + p.up_off + col) = *unit32(s + 1024, r, u);
             }
         }
         __syncwarp();
@@ -317,48 +342,95 @@ __device__ __forceinline__ void act_tile(const GParams& p, uint32_t tl, int m0, 
     }
 }
 
-struct Tile { int g, mt, nt, row0, mrows; };
+struct Tile { int g, m0, n0, row0, mrows; };
 
-template <int KIND>
-__device__ __forceinline__ Tile decode_tile(int tile, const int* prefix, const int* rstart, const int* rcount,
-                                            int groups, int ntm, int ntn) {
-    Tile t;
-    int local, mtiles;
-    if (KIND == kWeights) {
-        const int per = ntm * ntn;
-        t.g = tile / per;
-        local = tile - t.g * per;
-        mtiles = ntm;
-    } else {
-        int lo = 0, hi = groups;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (prefix[mid] <= tile) lo = mid; else hi = mid;
-        }
-        t.g = lo;
-        local = tile - prefix[lo];
-        mtiles = (rcount[lo] + TM - 1) / TM;
+// Tile `local` of a group of mtiles row tiles: bands of kBand column tiles, row
+// tiles first inside a band, so the tiles in flight share their operands in L2.
+__device__ __forceinline__ void place(Tile& t, int local, int mtiles) {
+    if (mtiles == 1) {           // a small group: no division
+        t.m0 = 0;
+        t.n0 = local * TN;
+        return;
     }
     const int band = local / (mtiles * kBand);
     const int idx = local - band * mtiles * kBand;
-    t.mt = idx % mtiles;
-    t.nt = band * kBand + idx / mtiles;
-    t.row0 = rstart[t.g];
-    t.mrows = rcount[t.g];
+    const int nt = idx / mtiles;
+    t.m0 = (idx - nt * mtiles) * TM;
+    t.n0 = (band * kBand + nt) * TN;
+}
+
+__device__ __forceinline__ Tile rows_tile(int tile, const int* prefix, const int* rstart, const int* rcount, int groups) {
+    int lo = 0, hi = groups;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= tile) lo = mid; else hi = mid;
+    }
+    Tile t;
+    t.g = lo;
+    t.row0 = rstart[lo];
+    t.mrows = rcount[lo];
+    place(t, tile - prefix[lo], (t.mrows + TM - 1) / TM);
     return t;
 }
 
-template <int KIND>
+__device__ __forceinline__ Tile weights_tile(int tile, const int* rstart, const int* rcount, int ntm, int ntn) {
+    Tile t;
+    t.g = tile / (ntm * ntn);
+    t.row0 = rstart[t.g];
+    t.mrows = rcount[t.g];
+    place(t, tile - t.g * ntm * ntn, ntm);
+    return t;
+}
+
+// The tiles of one CTA pair, the same for every role: first the rows form's, dealt
+// round; the `extra` pairs that got one more of them than the rest then sit out the
+// first `skip` rounds of the (mostly shorter) weights form's tiles, as many as take
+// about as long as that tile: the loop adds up their steps, five at least, which is
+// what writing a tile takes.
+struct Walk {
+    int nrows, total, pairs, pair, extra, skip, i, s, j;
+    __device__ __forceinline__ Walk(int nrows_, int total_, int pairs_, int pair_, int row_steps, int per_group,
+                                    const int* rcount)
+        : nrows(nrows_), total(total_), pairs(pairs_), pair(pair_), skip(0), i(pair_), s(0) {
+        extra = nrows % pairs;
+        if (extra)
+            for (int steps = 0; nrows + skip * pairs < total; ++skip) {
+                const int mine = max((rcount[skip * pairs / per_group] + BK - 1) / BK, 5);
+                if (steps + mine / 2 >= row_steps) break;
+                steps += mine;
+            }
+        j = nrows + skip * (pairs - extra) + pair;
+    }
+    __device__ __forceinline__ int next() {                       // -1: done
+        int t;
+        if (i < nrows) {
+            t = i;
+            i += pairs;
+            return t;
+        }
+        if (s < skip && pair >= extra) {
+            t = nrows + s * (pairs - extra) + pair - extra;
+            ++s;
+        } else {
+            t = j;
+            j += pairs;
+        }
+        return t < total ? t : -1;
+    }
+};
+
+template <int ACT>
 __global__ void __launch_bounds__(THREADS, 1)
 grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmWA, const __grid_constant__ CUtensorMap tmWB,
                       const GParams p) {
-    constexpr bool kW = KIND == kWeights;
+    const int stages = p.stages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
-    uint8_t* epi_smem = smem + STAGES * STAGE_BYTES;
+    uint8_t* epi_smem = smem + stages * STAGE_BYTES;
     Ctl* ctl = reinterpret_cast<Ctl*>(epi_smem + EPI_WARPS * EPI_BYTES);
-    int* prefix = reinterpret_cast<int*>(ctl + 1);
+    int* prefix = reinterpret_cast<int*>(ctl + 1);          // rows form: tiles before group g
     int* rstart = prefix + (p.groups + 1);
     int* rcount = rstart + p.groups;
     const uint32_t smem_base = smem_u32(smem);
@@ -366,10 +438,11 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();                 // 0: leader, 1: peer
     const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
-    const int ntn = (p.N + TN - 1) / TN, ntm = kW ? (p.M + TM - 1) / TM : 0;
+    const int ntn = (p.N + TN - 1) / TN;
+    const int wtm = (p.wM + TM - 1) / TM, wtn = (p.wN + TN - 1) / TN;
 
     if (tid == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(smem_u32(&ctl->full[s]), 1);
             mbar_init(smem_u32(&ctl->empty[s]), 1);
             mbar_init(smem_u32(&ctl->part[s]), 1);
@@ -385,11 +458,17 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
         fence_proxy_async_smem();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmWA);
+        tma_prefetch_desc(&tmWB);
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&ctl->tmem_base), TMEM_COLS);
         tmem_relinquish_pair();
     }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();              // both CTAs' barriers are initialised before any cross-CTA arrive
+    tc_fence_after();
     pdl_wait();
     pdl_trigger();
     // each bucket is clamped to [0, a_rows], so malformed offsets stay in bounds
@@ -401,8 +480,8 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
         rcount[g] = hi - lo;
     }
     __syncthreads();
-    if (!kW) {
-        // exclusive scan of tiles per group -> prefix[0..groups]
+    {
+        // exclusive scan of the rows form's tiles per group -> prefix[0..groups]
         const int n = p.groups;
         const int per = (n + THREADS - 1) / THREADS;
         const int g0 = tid * per;
@@ -426,18 +505,14 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 run += ((rcount[g0 + i] + TM - 1) / TM) * ntn;
             }
         }
-        if (tid == THREADS - 1) { prefix[n] = run; ctl->total_tiles = run; }
-    } else if (tid == 0) {
-        ctl->total_tiles = p.groups * ntm * ntn;
+        if (tid == THREADS - 1) { prefix[n] = run; ctl->rows_tiles = run; }
     }
-    tc_fence_before();
     __syncthreads();
-    cluster_sync();              // both CTAs' barriers are initialised before any cross-CTA arrive
-    tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
-    const int total = ctl->total_tiles;
     volatile int* abort = &ctl->abort;
     const int nk_rows = (p.K + BK - 1) / BK;
+    const int nrows = ctl->rows_tiles;
+    Walk walk(nrows, nrows + p.groups * wtm * wtn, npairs, pair, nk_rows, wtm * wtn, rcount);
 
     if (warp == 0) {
         // ---------------- TMA producer (both CTAs) ----------------
@@ -446,47 +521,55 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             uint32_t ph = 0;
             bool ok = true;
             long long armed = 0;
-            for (int tile = pair; tile < total && ok; tile += npairs) {
-                const Tile t = decode_tile<KIND>(tile, prefix, rstart, rcount, p.groups, ntm, ntn);
-                const int nk = kW ? (t.mrows + BK - 1) / BK : nk_rows;
-                const int a0 = t.mt * TM + (int)rank * HALF;     // A's row (rows form) or column
-                const int b0 = t.nt * TN + (int)rank * HALF;
-                for (int i = 0; i < nk; ++i) {
-                    if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), ph ^ 1u, abort)) { ok = false; break; }
-                    const uint32_t full_local = smem_u32(&ctl->full[stage]);
-                    const uint32_t full_leader = mapa_shared(full_local, 0);
-                    const uint32_t sa = smem_base + stage * STAGE_BYTES, sb = sa + OP_BYTES;
-                    if (kW) {
-                        const int y = t.row0 + i * BK;
-                        if (t.mrows - i * BK < BK) {
-                            // partial step: counted on this CTA's own barrier, for its fixer
-                            const uint32_t part = smem_u32(&ctl->part[stage]);
-                            mbar_arrive_expect_tx(part, STAGE_BYTES);
-                            tma_load_2d(sa, &tmA, part, a0, y);
-                            tma_load_2d(sa + BOX_BYTES, &tmA, part, a0 + 64, y);
-                            tma_load_2d(sb, &tmB, part, b0, y);
-                            tma_load_2d(sb + BOX_BYTES, &tmB, part, b0 + 64, y);
+            for (int tile; ok && (tile = walk.next()) >= 0;) {
+                const bool weights = tile >= nrows;
+                const Tile t = weights ? weights_tile(tile - nrows, rstart, rcount, wtm, wtn)
+                                       : rows_tile(tile, prefix, rstart, rcount, p.groups);
+                const int a0 = t.m0 + (int)rank * HALF;          // A's row (rows form) or column
+                const int b0 = t.n0 + (int)rank * HALF;
+                // one loop for each form: a step has 512 cycles, and one thread issues it
+                auto load = [&](auto form) {
+                    constexpr bool kW = decltype(form)::value;
+                    const int nk = kW ? (t.mrows + BK - 1) / BK : nk_rows;
+                    for (int i = 0; i < nk; ++i) {
+                        if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), ph ^ 1u, abort)) { ok = false; break; }
+                        const uint32_t full_local = smem_u32(&ctl->full[stage]);
+                        const uint32_t full_leader = mapa_shared(full_local, 0);
+                        const uint32_t sa = smem_base + stage * STAGE_BYTES, sb = sa + OP_BYTES;
+                        if (kW) {
+                            const int y = t.row0 + i * BK;
+                            if (t.mrows - i * BK < BK) {
+                                // partial step: counted on this CTA's own barrier, for its fixer
+                                const uint32_t part = smem_u32(&ctl->part[stage]);
+                                mbar_arrive_expect_tx(part, STAGE_BYTES);
+                                tma_load_2d(sa, &tmWA, part, a0, y);
+                                tma_load_2d(sa + BOX_BYTES, &tmWA, part, a0 + 64, y);
+                                tma_load_2d(sb, &tmWB, part, b0, y);
+                                tma_load_2d(sb + BOX_BYTES, &tmWB, part, b0 + 64, y);
+                            } else {
+                                if (rank == 0) mbar_arrive_expect_tx(full_local, 2 * STAGE_BYTES);
+                                tma_load_2d_pair(sa, &tmWA, full_leader, a0, y);
+                                tma_load_2d_pair(sa + BOX_BYTES, &tmWA, full_leader, a0 + 64, y);
+                                tma_load_2d_pair(sb, &tmWB, full_leader, b0, y);
+                                tma_load_2d_pair(sb + BOX_BYTES, &tmWB, full_leader, b0 + 64, y);
+                            }
                         } else {
                             if (rank == 0) mbar_arrive_expect_tx(full_local, 2 * STAGE_BYTES);
-                            tma_load_2d_pair(sa, &tmA, full_leader, a0, y);
-                            tma_load_2d_pair(sa + BOX_BYTES, &tmA, full_leader, a0 + 64, y);
-                            tma_load_2d_pair(sb, &tmB, full_leader, b0, y);
-                            tma_load_2d_pair(sb + BOX_BYTES, &tmB, full_leader, b0 + 64, y);
+                            tma_load_2d_pair(sa, &tmA, full_leader, i * BK, t.row0 + a0);
+                            tma_load_3d_pair(sb, &tmB, full_leader, b0, i * BK, t.g);
+                            tma_load_3d_pair(sb + BOX_BYTES, &tmB, full_leader, b0 + 64, i * BK, t.g);
                         }
-                    } else {
-                        if (rank == 0) mbar_arrive_expect_tx(full_local, 2 * STAGE_BYTES);
-                        tma_load_2d_pair(sa, &tmA, full_leader, i * BK, t.row0 + a0);
-                        tma_load_3d_pair(sb, &tmB, full_leader, b0, i * BK, t.g);
-                        tma_load_3d_pair(sb + BOX_BYTES, &tmB, full_leader, b0 + 64, i * BK, t.g);
+                        ++armed;
+                        if (++stage == stages) { stage = 0; ph ^= 1u; }
                     }
-                    ++armed;
-                    if (++stage == STAGES) { stage = 0; ph ^= 1u; }
-                }
+                };
+                if (weights) load(std::true_type{});
+                else load(std::false_type{});
             }
             if (!ok) {
                 // as in the forward pair kernel: the leader waits for the phases it
                 // armed, the peer (which cannot wait on a remote barrier) adds a delay
-                if (rank != 0 || !wait_armed_stages(smem_u32(&ctl->full[0]), STAGES, armed)) settle_delay();
+                if (rank != 0 || !wait_armed_stages(smem_u32(&ctl->full[0]), stages, armed)) settle_delay();
                 raise_status(p.hdr, MOE_ERR_TIMEOUT);
                 p.hdr->timeout_site = kSiteGradProducer;
             }
@@ -494,40 +577,40 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     } else if (warp == 1) {
         // ---------------- MMA issuer (leader CTA) ----------------
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = idesc_bf16_f32(TM, TN) | kMajorB | (kW ? kMajorA : 0u);
-            constexpr uint64_t astep = kW ? kMnStep : kKStep;
             int stage = 0;
             uint32_t ph = 0;
             int acc = 0;
             uint32_t aph = 0;
             bool ok = true;
-            for (int tile = pair; tile < total && ok; tile += npairs) {
-                const Tile t = decode_tile<KIND>(tile, prefix, rstart, rcount, p.groups, ntm, ntn);
-                const int nk = kW ? (t.mrows + BK - 1) / BK : nk_rows;
-                if (nk == 0) continue;
-                if (!mbar_wait_bounded(smem_u32(&ctl->tempty[acc]), aph ^ 1u, abort)) { ok = false; break; }
+            for (int tile; ok && (tile = walk.next()) >= 0;) {
+                const bool weights = tile >= nrows;
+                const int mrows = weights ? rcount[(tile - nrows) / (wtm * wtn)] : 1;
+                if (mrows == 0) continue;
+                if (!mbar_wait_cluster(smem_u32(&ctl->tempty[acc]), aph ^ 1u, abort)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(acc * TN);
-                for (int i = 0; i < nk; ++i) {
-                    const uint32_t full = smem_u32(&ctl->full[stage]);
-                    const int left = kW ? t.mrows - i * BK : BK;
-                    // a partial step: the other CTA's fixer wrote its shared memory
-                    if (!(kW && left < BK ? mbar_wait_cluster(full, ph, abort) : mbar_wait_bounded(full, ph, abort))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = smem_base + stage * STAGE_BYTES;
-                    const uint64_t ad = kW ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
-                    const uint64_t bd = sdesc_mn_sw128(sa + OP_BYTES);
+                auto multiply = [&](auto form) {
+                    constexpr bool kW = decltype(form)::value;
+                    constexpr uint32_t idesc = idesc_bf16_f32(TM, TN) | kMajorB | (kW ? kMajorA : 0u);
+                    constexpr uint64_t astep = kW ? kMnStep : kKStep;
+                    const int nk = kW ? (mrows + BK - 1) / BK : nk_rows;
+                    for (int i = 0; i < nk; ++i) {
+                        if (!mbar_wait_bounded(smem_u32(&ctl->full[stage]), ph, abort)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t sa = smem_base + stage * STAGE_BYTES;
+                        const uint64_t ad = kW ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
+                        const uint64_t bd = sdesc_mn_sw128(sa + OP_BYTES);
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk)
-                        if (!kW || kk * 16 < left)
-                            tc_mma_bf16_pair(d, ad + (uint64_t)kk * astep, bd + (uint64_t)kk * kMnStep, idesc,
-                                             (i > 0 || kk > 0) ? 1u : 0u);
-                    tc_commit_pair_mc(smem_u32(&ctl->empty[stage]), (uint16_t)3);
-                    if (++stage == STAGES) { stage = 0; ph ^= 1u; }
-                }
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            if (!kW || i * BK + kk * 16 < mrows)          // slices that hold rows
+                                tc_mma_bf16_pair(d, ad + (uint64_t)kk * astep, bd + (uint64_t)kk * kMnStep, idesc,
+                                                 (i > 0 || kk > 0) ? 1u : 0u);
+                        tc_commit_pair_mc(smem_u32(&ctl->empty[stage]), (uint16_t)3);
+                        if (++stage == stages) { stage = 0; ph ^= 1u; }
+                    }
+                };
+                if (weights) multiply(std::true_type{});
+                else multiply(std::false_type{});
                 if (!ok) break;
                 tc_commit_pair_mc(smem_u32(&ctl->tfull[acc]), (uint16_t)3);
                 acc ^= 1;
@@ -543,19 +626,21 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             }
         }
     } else if (warp < 2 + EPI_WARPS) {
-        // ---------------- epilogue (both CTAs): a warp = 32 rows of the tile ----------------
-        const int q = warp & 3;
-        uint8_t* epi = epi_smem + q * EPI_BYTES;
+        // ---------------- epilogue (both CTAs): a warp = 32 rows x EPI_COLS columns ----------------
+        const int q = warp & 3;                                      // the TMEM lanes a warp can read
+        const int c0 = (warp - 2) / 4 * EPI_COLS;
+        uint8_t* epi = epi_smem + (warp - 2) * EPI_BYTES;
         int acc = 0;
         uint32_t aph = 0;
-        for (int tile = pair; tile < total; tile += npairs) {
-            const Tile t = decode_tile<KIND>(tile, prefix, rstart, rcount, p.groups, ntm, ntn);
-            const int m0 = t.mt * TM + (int)rank * HALF + q * 32;      // this warp's 32 rows
-            const int rows = (kW ? p.M : t.mrows) - m0;                // of which below the bound
-            const int n0 = t.nt * TN;
-            const bool empty = kW && t.mrows == 0;
-            if (KIND == kRowsSwiGLU || KIND == kRowsReLU2)
-                act_prefetch<KIND == kRowsSwiGLU>(p, m0, rows, t.row0, n0, epi, lane);
+        for (int tile; (tile = walk.next()) >= 0;) {
+            const bool weights = tile >= nrows;
+            const Tile t = weights ? weights_tile(tile - nrows, rstart, rcount, wtm, wtn)
+                                   : rows_tile(tile, prefix, rstart, rcount, p.groups);
+            const int m0 = t.m0 + (int)rank * HALF + q * 32;
+            const int rows = (weights ? p.wM : t.mrows) - m0;            // of its 32 rows, those below the bound
+            const int n0 = t.n0 + c0;
+            const bool empty = weights && t.mrows == 0;                  // zeros, no accumulator
+            if (ACT != kPlain && !weights) act_prefetch<ACT == kSwiGLU>(p, m0, rows, t.row0, n0, epi, lane);
             if (!empty) {
                 if (!mbar_wait_bounded(smem_u32(&ctl->tfull[acc]), aph, abort)) {
                     if (lane == 0) {
@@ -566,39 +651,44 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 }
                 tc_fence_after();
             }
-            const uint32_t tl = tmem_base + (uint32_t)(acc * TN) + ((uint32_t)(q * 32) << 16);
+            const uint32_t tl = tmem_base + (uint32_t)(acc * TN + c0) + ((uint32_t)(q * 32) << 16);
             auto release = [&] {               // the accumulator is read: the next tile may overwrite it
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&ctl->tempty[acc]), 0));
+                if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&ctl->tempty[acc]), 0));
             };
-            if (KIND == kRowsSwiGLU || KIND == kRowsReLU2) {
-                act_tile<KIND == kRowsSwiGLU>(p, tl, m0, rows, t.row0, n0, epi, lane, release);
-            } else if (kW && p.wmode != MOE_WGRAD_BF16) {
+            if (weights && p.wmode != MOE_WGRAD_BF16) {
                 if (!(empty && p.wmode == MOE_WGRAD_F32_ADD))
-                    f32_tile(p, tl, empty, rows, n0, static_cast<float*>(p.out) + ((size_t)t.g * p.M + m0) * p.ldo, epi,
-                             lane, release);
+                    f32_tile(p, tl, empty, rows, n0,
+                             static_cast<float*>(p.wout) + ((size_t)t.g * p.wM + m0) * p.wN, epi, lane, release);
+            } else if (ACT != kPlain && !weights) {
+                act_tile<ACT == kSwiGLU>(p, tl, m0, rows, t.row0, n0, epi, lane, release);
             } else {
-                const size_t row = kW ? (size_t)t.g * p.M + m0 : (size_t)(t.row0 + m0);
-                bf16_tile(tl, empty, rows, n0, p.N, static_cast<__nv_bfloat16*>(p.out) + row * p.ldo, p.ldo, epi, lane,
-                          release);
+                const int N = weights ? p.wN : p.N;
+                const long long ldo = weights ? (long long)p.wN : p.ldo;
+                __nv_bfloat16* out = weights ? static_cast<__nv_bfloat16*>(p.wout) + ((size_t)t.g * p.wM + m0) * p.wN
+                                             : p.out + (size_t)(t.row0 + m0) * p.ldo;
+                bf16_tile(tl, empty, rows, n0, N, out, ldo, epi, lane, release);
             }
             if (empty) continue;
             acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-    } else if (kW) {
-        // ---------------- fixer (both CTAs): partial reduction steps ----------------
+    } else {
+        // ---------------- fixer (both CTAs): the weights form's partial steps ----------------
         int stage = 0;
         uint32_t pph = 0;                          // parity of part[s] and fixed[s] in bit s
         bool ok = true;
-        for (int tile = pair; tile < total && ok; tile += npairs) {
-            const Tile t = decode_tile<KIND>(tile, prefix, rstart, rcount, p.groups, ntm, ntn);
-            const int nk = (t.mrows + BK - 1) / BK;
-            const int rem = t.mrows & (BK - 1);
+        for (int tile; ok && (tile = walk.next()) >= 0;) {
+            int nk = nk_rows, rem = 0;
+            if (tile >= nrows) {
+                const int mrows = rcount[(tile - nrows) / (wtm * wtn)];
+                nk = (mrows + BK - 1) / BK;
+                rem = mrows & (BK - 1);
+            }
             if (rem) {
-                const int s = (stage + nk - 1) % STAGES;
+                const int s = (stage + nk - 1) % stages;
                 const uint32_t parity = (pph >> s) & 1u;
                 pph ^= 1u << s;
                 if (!mbar_wait_bounded(smem_u32(&ctl->part[s]), parity, abort)) { ok = false; break; }
@@ -612,13 +702,16 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (rank != 0) {
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->fixed[s]), 0));
+                    if (lane == 0) {
+                        fence_release_smem_cluster();
+                        mbar_arrive_relaxed(mapa_shared(smem_u32(&ctl->fixed[s]), 0));
+                    }
                 } else {
                     if (!mbar_wait_cluster(smem_u32(&ctl->fixed[s]), parity, abort)) { ok = false; break; }
-                    if (lane == 0) mbar_arrive_cluster(smem_u32(&ctl->full[s]));
+                    if (lane == 0) mbar_arrive(smem_u32(&ctl->full[s]));
                 }
             }
-            stage = (stage + nk) % STAGES;
+            stage = (stage + nk) % stages;
         }
         if (!ok && lane == 0) {
             raise_status(p.hdr, MOE_ERR_TIMEOUT);
@@ -636,25 +729,26 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     }
 }
 
-size_t smem_bytes(int groups) {
-    return 1024 + (size_t)STAGES * STAGE_BYTES + EPI_WARPS * EPI_BYTES + sizeof(Ctl) + 3 * (size_t)(groups + 1) * 4;
+size_t smem_bytes(int groups, int stages) {
+    return 1024 + (size_t)stages * STAGE_BYTES + EPI_WARPS * EPI_BYTES + sizeof(Ctl) + 3 * (size_t)(groups + 1) * 4;
 }
 
-template <int KIND>
-moe_status launch_kind(const CUtensorMap& ma, const CUtensorMap& mb, const GParams& gp, cudaStream_t st) {
+template <int ACT>
+moe_status launch_grad(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mwa, const CUtensorMap& mwb,
+                       const GParams& gp, cudaStream_t st) {
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(grad_gemm_pair_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr_err = cudaFuncSetAttribute(grad_gemm_pair_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         MAX_DYN_SMEM);
     });
     if (attr_err != cudaSuccess) {
         set_error("cudaFuncSetAttribute(max dynamic smem %d): %s", MAX_DYN_SMEM, cudaGetErrorString(attr_err));
         return MOE_ERR_CUDA;
     }
-    const size_t smem = smem_bytes(gp.groups);
-    const cudaError_t e = launch_kernel(grad_gemm_pair_kernel<KIND>, dim3((unsigned)(device_sm_count() & ~1)),
-                                        dim3(THREADS), smem, st, 2, kUsePdl, ma, mb, gp);
+    const size_t smem = smem_bytes(gp.groups, gp.stages);
+    const cudaError_t e = launch_kernel(grad_gemm_pair_kernel<ACT>, dim3((unsigned)(device_sm_count() & ~1)),
+                                        dim3(THREADS), smem, st, 2, kUsePdl, ma, mb, mwa, mwb, gp);
     if (e != cudaSuccess) {
         set_error("gradient GEMM launch (smem %zu): %s", smem, cudaGetErrorString(e));
         return MOE_ERR_CUDA;
@@ -698,51 +792,44 @@ act_kernel(long long rows, int IV, long long ldv, const int32_t* __restrict__ of
 
 }  // namespace
 
-moe_status launch_rows_grad(const RowsGradProblem& g, WsHeader* hdr, cudaStream_t st) {
-    const long long tiles = (g.rows / TM + g.groups) * (((long long)g.N + TN - 1) / TN);
-    if (device_sm_count() < 2 || tiles > INT_MAX / 2 || smem_bytes(g.groups) > (size_t)MAX_DYN_SMEM) {
+moe_status launch_expert_grad(const ExpertGradProblem& g, WsHeader* hdr, cudaStream_t st) {
+    const long long rows_tiles = g.out ? (g.rows / TM + g.groups) * (((long long)g.N + TN - 1) / TN) : 0;
+    const long long w_tiles = g.wout ? (long long)g.groups * ((g.wM + TM - 1) / TM) * ((g.wN + TN - 1) / TN) : 0;
+    if (device_sm_count() < 2 || rows_tiles + w_tiles > INT_MAX / 2 ||
+        smem_bytes(g.groups, MAX_STAGES - 1) > (size_t)MAX_DYN_SMEM) {
         set_error("gradient GEMM: unsupported problem (groups %d, K %d, N %d)", g.groups, g.K, g.N);
         return MOE_ERR_UNSUPPORTED;
     }
-    CUtensorMap ma, mb;
-    if (!make_tensor_map_bf16(&ma, g.a, g.rows, g.K, 128u)) return MOE_ERR_CUDA;
-    if (!make_tensor_map_bf16_groups(&mb, g.w, g.groups, g.K, g.N, 64u)) return MOE_ERR_CUDA;
+    CUtensorMap ma, mb, mwa, mwb;
     GParams gp{};
-    gp.offsets = g.offsets;
-    gp.groups = g.groups;
-    gp.a_rows = (int)g.rows;
-    gp.K = g.K;
-    gp.N = g.N;
-    gp.out = g.out;
-    gp.ldo = g.ldo;
-    gp.pre = reinterpret_cast<const __nv_bfloat16*>(g.pre);
-    gp.ldp = g.ldo;
-    gp.up_off = g.N;
-    gp.hdr = hdr;
-    if (!g.pre) return launch_kind<kRowsPlain>(ma, mb, gp, st);
-    return g.act == MOE_ACT_SWIGLU ? launch_kind<kRowsSwiGLU>(ma, mb, gp, st) : launch_kind<kRowsReLU2>(ma, mb, gp, st);
-}
-
-moe_status launch_weights_grad(const WeightsGradProblem& g, WsHeader* hdr, cudaStream_t st) {
-    const long long tiles = (long long)g.groups * ((g.M + TM - 1) / TM) * ((g.N + TN - 1) / TN);
-    if (device_sm_count() < 2 || tiles > INT_MAX / 2 || smem_bytes(g.groups) > (size_t)MAX_DYN_SMEM) {
-        set_error("weight-gradient GEMM: unsupported problem (groups %d, M %d, N %d)", g.groups, g.M, g.N);
-        return MOE_ERR_UNSUPPORTED;
+    if (g.out) {
+        if (!make_tensor_map_bf16(&ma, g.a, g.rows, g.K, 128u)) return MOE_ERR_CUDA;
+        if (!make_tensor_map_bf16_groups(&mb, g.w, g.groups, g.K, g.N, 64u)) return MOE_ERR_CUDA;
+        gp.K = g.K;
+        gp.N = g.N;
+        gp.out = reinterpret_cast<__nv_bfloat16*>(g.out);
+        gp.ldo = g.ldo;
+        gp.pre = reinterpret_cast<const __nv_bfloat16*>(g.pre);
+        gp.up_off = g.N;
     }
-    CUtensorMap ma, mb;
-    if (!make_tensor_map_bf16(&ma, g.a, g.rows, g.M, 64u) || !make_tensor_map_bf16(&mb, g.b, g.rows, g.N, 64u))
-        return MOE_ERR_CUDA;
-    GParams gp{};
+    if (g.wout) {
+        if (!make_tensor_map_bf16(&mwa, g.a, g.rows, g.wM, 64u) || !make_tensor_map_bf16(&mwb, g.wb, g.rows, g.wN, 64u))
+            return MOE_ERR_CUDA;
+        gp.wM = g.wM;
+        gp.wN = g.wN;
+        gp.wmode = g.wmode;
+        gp.wout = g.wout;
+    }
+    if (!g.out) { ma = mwa; mb = mwb; }        // a form not asked for has no tiles: its maps are not used
+    if (!g.wout) { mwa = ma; mwb = mb; }
     gp.offsets = g.offsets;
     gp.groups = g.groups;
     gp.a_rows = (int)g.rows;
-    gp.M = g.M;
-    gp.N = g.N;
-    gp.out = g.out;
-    gp.ldo = g.N;
-    gp.wmode = g.wmode;
+    gp.stages = smem_bytes(g.groups, MAX_STAGES) <= (size_t)MAX_DYN_SMEM ? MAX_STAGES : MAX_STAGES - 1;
     gp.hdr = hdr;
-    return launch_kind<kWeights>(ma, mb, gp, st);
+    if (!g.out || !g.pre) return launch_grad<kPlain>(ma, mb, mwa, mwb, gp, st);
+    return g.act == MOE_ACT_SWIGLU ? launch_grad<kSwiGLU>(ma, mb, mwa, mwb, gp, st)
+                                   : launch_grad<kReLU2>(ma, mb, mwa, mwb, gp, st);
 }
 
 cudaError_t launch_act(const moe_shape& s, const int32_t* offsets, const uint16_t* pre, uint16_t* h, cudaStream_t st) {
