@@ -357,7 +357,7 @@ MOE_API moe_status moe_ep_plan(int32_t experts, int32_t world, int32_t rank, int
  * The forward chain is layer norm -> gate -> route -> dispatch ->
  * moe_expert_up_train -> moe_expert_down -> moe_combine; the calls below are the
  * layer norm, the up projection that keeps what its gradient needs, and the
- * gradients.  The library's conventions hold: contiguous row-major buffers of the
+ * gradients of each. The library's conventions hold: contiguous row-major buffers of the
  * caller, 16-byte aligned, work enqueued on `stream`, nothing allocated.  No
  * gradient is summed with atomics: results do not change from run to run. */
 
@@ -427,6 +427,18 @@ MOE_API moe_status moe_route_backward(const moe_shape* shape, const int32_t* top
 MOE_API moe_status moe_route_sigmoid_backward(const moe_shape* shape, const float* logits, const int32_t* topk_ids,
                                               float route_scale, const float* dtopk_w, float* dlogits, void* ws,
                                               size_t ws_bytes, void* stream);
+
+/* Gradient of moe_gate:
+ *   dx      = bf16(g w_gate),  dw_gate = sum_t g[t]^T x[t],  g = bf16(dlogits)
+ * with FP32 accumulation (dlogits is rounded once, as every gradient the GEMMs read).
+ *   dlogits      device f32 [T, E]; x device bf16 [T, H]; w_gate device bf16 [E, H]
+ *   dlogits_bf16 device bf16 [T, 8 * ceil(E / 8)] out: g, zeros past column E
+ *   dx      device bf16 [T, H] out (`add` of moe_dispatch_backward), or NULL: w_gate is not read
+ *   dw_gate device [E, H] out, bf16 or f32 as `wgrad` says, or NULL: x is not read
+ * Host error: MOE_ERR_INVALID_ARG when both outputs are NULL. */
+MOE_API moe_status moe_gate_backward(const moe_shape* shape, const float* dlogits, const uint16_t* x,
+                                     const uint16_t* w_gate, uint16_t* dlogits_bf16, uint16_t* dx, void* dw_gate,
+                                     int32_t wgrad, void* ws, size_t ws_bytes, void* stream);
 
 /* moe_expert_up that also keeps its pre-activations (no shared experts):
  *   pre device bf16 [T*k, up] out: bf16(x_perm W13[e]^T), FP32 accumulation

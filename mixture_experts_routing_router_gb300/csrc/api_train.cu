@@ -147,6 +147,30 @@ moe_status moe_route_sigmoid_backward(const moe_shape* shape, const float* logit
                                        static_cast<cudaStream_t>(stream)));
 }
 
+moe_status moe_gate_backward(const moe_shape* shape, const float* dlogits, const uint16_t* x, const uint16_t* w_gate,
+                             uint16_t* dlogits_bf16, uint16_t* dx, void* dw_gate, int32_t wgrad, void* ws,
+                             size_t ws_bytes, void* stream) {
+    clear_error();
+    moe_status r = check_stage(shape, ws, ws_bytes);
+    if (r != MOE_OK) return r;
+    if (!aligned(dlogits, 16) || !aligned(dlogits_bf16, 16) || (!dx && !dw_gate) || !is_wgrad(wgrad))
+        return MOE_ERR_INVALID_ARG;
+    if (dx && (!aligned(dx, 16) || !aligned(w_gate, 16))) return MOE_ERR_INVALID_ARG;
+    if (dw_gate && (!aligned(dw_gate, 16) || !aligned(x, 16))) return MOE_ERR_INVALID_ARG;
+    const moe_shape& s = *shape;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int cols = (s.experts + 7) / 8 * 8;      // TMA rows are multiples of 16 bytes
+    if ((r = from_cuda(launch_round_rows(s.tokens, s.experts, cols, dlogits, dlogits_bf16, st))) != MOE_OK) return r;
+    ExpertGradProblem g{};
+    g.a = dlogits_bf16; g.rows = s.tokens; g.a_cols = cols;
+    g.offsets = nullptr; g.groups = 1;
+    g.w = w_gate; g.K = s.experts; g.N = s.hidden;
+    g.out = dx; g.ldo = s.hidden;
+    g.wb = x; g.wM = s.experts; g.wN = s.hidden;
+    g.wout = dw_gate; g.wmode = wgrad;
+    return launch_expert_grad(g, header(ws), st);
+}
+
 moe_status moe_expert_up_train(const moe_shape* shape, const uint16_t* x_perm, const int32_t* offsets,
                                const uint16_t* w13, uint16_t* pre, uint16_t* h, void* ws, size_t ws_bytes,
                                void* stream) {
@@ -182,7 +206,7 @@ moe_status moe_expert_down_backward(const moe_shape* shape, const uint16_t* dy_p
     if (dw2 && (!aligned(dw2, 16) || !aligned(h, 16))) return MOE_ERR_INVALID_ARG;
     const moe_shape& s = *shape;
     ExpertGradProblem g{};
-    g.a = dy_perm; g.rows = (long long)s.tokens * s.top_k;
+    g.a = dy_perm; g.rows = (long long)s.tokens * s.top_k; g.a_cols = s.hidden;
     g.offsets = offsets; g.groups = s.experts;
     g.w = w2; g.K = s.hidden; g.N = s.inter;
     g.out = dpre; g.ldo = up_rows(s);
@@ -203,7 +227,7 @@ moe_status moe_expert_up_backward(const moe_shape* shape, const uint16_t* dpre, 
     if (dw13 && (!aligned(dw13, 16) || !aligned(x_perm, 16))) return MOE_ERR_INVALID_ARG;
     const moe_shape& s = *shape;
     ExpertGradProblem g{};
-    g.a = dpre; g.rows = (long long)s.tokens * s.top_k;
+    g.a = dpre; g.rows = (long long)s.tokens * s.top_k; g.a_cols = up_rows(s);
     g.offsets = offsets; g.groups = s.experts;
     g.w = w13; g.K = up_rows(s); g.N = s.hidden;
     g.out = dx_perm; g.ldo = s.hidden;

@@ -602,15 +602,17 @@ cudaError_t launch_act(const moe_shape& s, const int32_t* offsets, const uint16_
 //   weights form (wout): C[g][m, n] = sum over the rows r of group g of a[r, m] wb[r, n],
 //                        stored as the moe_wgrad value wmode says.
 struct ExpertGradProblem {
-    const uint16_t* a; long long rows;
-    const int32_t* offsets; int groups;
+    const uint16_t* a; long long rows; int a_cols;   // a_cols: row length, a multiple of 8, K and wM at most
+    const int32_t* offsets; int groups;              // offsets NULL: one group of all rows
     const uint16_t* w; int K, N;
     uint16_t* out; long long ldo;
     const uint16_t* pre; int act;
-    const uint16_t* wb; int wM, wN;      // wM == K: a's columns
+    const uint16_t* wb; int wM, wN;
     void* wout; int wmode;
 };
 moe_status launch_expert_grad(const ExpertGradProblem& p, WsHeader* hdr, cudaStream_t st);
+// FP32 [rows, cols] to BF16 [rows, cols8], zeros past cols.
+cudaError_t launch_round_rows(long long rows, int cols, int cols8, const float* a, uint16_t* b, cudaStream_t st);
 
 int device_sm_count();
 

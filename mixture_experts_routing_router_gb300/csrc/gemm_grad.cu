@@ -56,7 +56,7 @@ constexpr int kBand = 8;                          // column tiles per band of th
 constexpr int MAX_DYN_SMEM = 232448 - 1024;       // the opt-in limit less the kernel's static part
 
 struct GParams {
-    const int32_t* offsets;
+    const int32_t* offsets;          // NULL: one group of all rows
     int groups, a_rows;              // bucket bounds are clamped to [0, a_rows]
     int stages;                      // of the shared-memory ring
     WsHeader* hdr;
@@ -473,7 +473,7 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     pdl_trigger();
     // each bucket is clamped to [0, a_rows], so malformed offsets stay in bounds
     for (int g = tid; g < p.groups; g += THREADS) {
-        int lo = p.offsets[g], hi = p.offsets[g + 1];
+        int lo = p.offsets ? p.offsets[g] : 0, hi = p.offsets ? p.offsets[g + 1] : p.a_rows;
         lo = lo < 0 ? 0 : (lo > p.a_rows ? p.a_rows : lo);
         hi = hi < lo ? lo : (hi > p.a_rows ? p.a_rows : hi);
         rstart[g] = lo;
@@ -756,6 +756,18 @@ moe_status launch_grad(const CUtensorMap& ma, const CUtensorMap& mb, const CUten
     return MOE_OK;
 }
 
+// FP32 [rows, cols] to BF16 [rows, cols8], the columns past cols zero.
+__global__ void __launch_bounds__(256)
+round_rows_kernel(long long n, int cols, int cols8, const float* __restrict__ a, __nv_bfloat16* __restrict__ b) {
+    pdl_wait();
+    pdl_trigger();
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+        const long long r = i / cols8;
+        const int c = (int)(i - r * cols8);
+        b[i] = __float2bfloat16_rn(c < cols ? a[r * cols + c] : 0.f);
+    }
+}
+
 // h = bf16(act(pre)) for the valid rows; eight columns a thread.
 template <bool GLU>
 __global__ void __launch_bounds__(256)
@@ -803,7 +815,7 @@ moe_status launch_expert_grad(const ExpertGradProblem& g, WsHeader* hdr, cudaStr
     CUtensorMap ma, mb, mwa, mwb;
     GParams gp{};
     if (g.out) {
-        if (!make_tensor_map_bf16(&ma, g.a, g.rows, g.K, 128u)) return MOE_ERR_CUDA;
+        if (!make_tensor_map_bf16(&ma, g.a, g.rows, g.a_cols, 128u)) return MOE_ERR_CUDA;
         if (!make_tensor_map_bf16_groups(&mb, g.w, g.groups, g.K, g.N, 64u)) return MOE_ERR_CUDA;
         gp.K = g.K;
         gp.N = g.N;
@@ -813,7 +825,7 @@ moe_status launch_expert_grad(const ExpertGradProblem& g, WsHeader* hdr, cudaStr
         gp.up_off = g.N;
     }
     if (g.wout) {
-        if (!make_tensor_map_bf16(&mwa, g.a, g.rows, g.wM, 64u) || !make_tensor_map_bf16(&mwb, g.wb, g.rows, g.wN, 64u))
+        if (!make_tensor_map_bf16(&mwa, g.a, g.rows, g.a_cols, 64u) || !make_tensor_map_bf16(&mwb, g.wb, g.rows, g.wN, 64u))
             return MOE_ERR_CUDA;
         gp.wM = g.wM;
         gp.wN = g.wN;
@@ -830,6 +842,15 @@ moe_status launch_expert_grad(const ExpertGradProblem& g, WsHeader* hdr, cudaStr
     if (!g.out || !g.pre) return launch_grad<kPlain>(ma, mb, mwa, mwb, gp, st);
     return g.act == MOE_ACT_SWIGLU ? launch_grad<kSwiGLU>(ma, mb, mwa, mwb, gp, st)
                                    : launch_grad<kReLU2>(ma, mb, mwa, mwb, gp, st);
+}
+
+cudaError_t launch_round_rows(long long rows, int cols, int cols8, const float* a, uint16_t* b, cudaStream_t st) {
+    const long long n = rows * cols8;
+    long long blocks = (n + 255) / 256;
+    const long long cap = (long long)device_sm_count() * 8;
+    if (blocks > cap) blocks = cap;
+    return launch_kernel(round_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, st, 1, kUsePdl, n, cols, cols8, a,
+                         reinterpret_cast<__nv_bfloat16*>(b));
 }
 
 cudaError_t launch_act(const moe_shape& s, const int32_t* offsets, const uint16_t* pre, uint16_t* h, cudaStream_t st) {

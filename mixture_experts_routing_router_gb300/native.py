@@ -44,7 +44,7 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_dispatc
            "moe_expert_up_nvfp4", "moe_expert_down_nvfp4", "moe_layer_nvfp4", "moe_workspace_set_wait",
            "moe_timeout_site_read", "moe_ep_plan", "moe_layernorm", "moe_layernorm_scratch_size",
            "moe_layernorm_backward", "moe_combine_backward", "moe_dispatch_backward", "moe_route_backward",
-           "moe_route_sigmoid_backward", "moe_expert_up_train", "moe_expert_down_backward",
+           "moe_route_sigmoid_backward", "moe_gate_backward", "moe_expert_up_train", "moe_expert_down_backward",
            "moe_expert_up_backward")
 
 
@@ -120,6 +120,7 @@ def lib():
                 "moe_dispatch_backward": [SP, P, P, P, P, P, S, P],
                 "moe_route_backward": [SP, P, P, P, P, P, S, P],
                 "moe_route_sigmoid_backward": [SP, P, P, ctypes.c_float, P, P, P, S, P],
+                "moe_gate_backward": [SP, P, P, P, P, P, P, I32, P, S, P],
                 "moe_expert_up_train": [SP, P, P, P, P, P, P, S, P],
                 "moe_expert_down_backward": [SP, P, P, P, P, P, P, P, I32, P, S, P],
                 "moe_expert_up_backward": [SP, P, P, P, P, P, P, I32, P, S, P],
@@ -395,12 +396,6 @@ def moe_route_sigmoid_backward(shape, logits, topk_ids, route_scale, dtopk_w, dl
            "moe_route_sigmoid_backward")
 
 
-def moe_expert_up_train(shape, x_perm, offsets, w13, pre, h, ws, stream=None):
-    """Up projection that also keeps its pre-activations for the backward pass."""
-    _check(lib().moe_expert_up_train(ctypes.byref(shape), _ptr(x_perm), _ptr(offsets), _ptr(w13), _ptr(pre), _ptr(h),
-                                     _ptr(ws), _wsb(ws), _stream(stream)), "moe_expert_up_train")
-
-
 def _wgrad(dw, add):
     """The moe_wgrad value of a weight gradient's tensor."""
     if dw is None:
@@ -410,6 +405,20 @@ def _wgrad(dw, add):
     if add:
         raise ValueError("weight gradients are accumulated in float32")
     return MOE_WGRAD_BF16
+
+
+def moe_gate_backward(shape, dlogits, x, w_gate, dlogits_bf16, dx, dw_gate, ws, stream=None, add=False):
+    """dx (None: skipped) and dw_gate (None: skipped; bfloat16 or float32, `add` accumulates into
+    float32) from dlogits, rounded into dlogits_bf16 [T, 8 * ceil(E / 8)] on the way."""
+    _check(lib().moe_gate_backward(ctypes.byref(shape), _ptr(dlogits), _ptr(x), _ptr(w_gate), _ptr(dlogits_bf16),
+                                   _ptr(dx), _ptr(dw_gate), _wgrad(dw_gate, add), _ptr(ws), _wsb(ws),
+                                   _stream(stream)), "moe_gate_backward")
+
+
+def moe_expert_up_train(shape, x_perm, offsets, w13, pre, h, ws, stream=None):
+    """Up projection that also keeps its pre-activations for the backward pass."""
+    _check(lib().moe_expert_up_train(ctypes.byref(shape), _ptr(x_perm), _ptr(offsets), _ptr(w13), _ptr(pre), _ptr(h),
+                                     _ptr(ws), _wsb(ws), _stream(stream)), "moe_expert_up_train")
 
 
 def moe_expert_down_backward(shape, dy_perm, offsets, w2, pre, h, dpre, dw2, ws, stream=None, add=False):

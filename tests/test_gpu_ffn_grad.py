@@ -183,6 +183,32 @@ def test_up_train_keeps_its_pre_activations(counts, glu):
     check(h.t[:v], want, (ref.U_BF16 + e) * want.abs(), "h")
 
 
+@pytest.mark.parametrize("size", [(1, 8, 1), (5, 72, 3), (64, 256, 16), (300, 136, 33), (257, 1000, 240),
+                                  (130, 64, 1024), (2000, 520, 100)], ids=str)
+def test_gate_backward(size):
+    T, H, E = size
+    g = torch.Generator().manual_seed(T)
+    shape = N.make_shape(T, H, E, 1, 8)
+    ws = N.workspace(shape, dev())
+    dl = torch.randn(T, E, generator=g).to(dev())
+    x, w = (torch.randn(n, H, generator=g).to(BF16).to(dev()) for n in (T, E))
+    gb = Guarded((T, (E + 7) // 8 * 8), BF16)
+    dx, dw, dw32 = Guarded((T, H), BF16), Guarded((E, H), BF16), Guarded((E, H), F32)
+    N.moe_gate_backward(shape, dl, x, w, gb.t, dx.t, dw.t, ws)
+    assert N.moe_status_read(ws) == N.MOE_OK and all(b.intact() for b in (gb, dx, dw))
+    assert torch.equal(gb.t[:, :E], dl.to(BF16)) and torch.all(gb.t[:, E:] == 0)
+    gd, xd, wd = gb.t[:, :E].to(D), x.to(D), w.to(D)
+    want = gd @ wd
+    check(dx.t, want, ref.sum_bound(E, gd.abs() @ wd.abs()) + ref.U_BF16 * want.abs(), "dx")
+    want, mag = gd.t() @ xd, gd.abs().t() @ xd.abs()
+    check(dw.t, want, ref.sum_bound(T, mag) + ref.U_BF16 * want.abs(), "dw_gate")
+    old = torch.randn(E, H, device=dev())
+    dw32.t.copy_(old)
+    N.moe_gate_backward(shape, dl, x, None, gb.t, None, dw32.t, ws, add=True)
+    assert N.moe_status_read(ws) == N.MOE_OK and dw32.intact()
+    check(dw32.t, want + old.to(D), ref.sum_bound(T, mag) + 2 * ref.U_F32 * (want.abs() + old.to(D).abs()), "dw_gate +=")
+
+
 def test_runs_on_the_given_stream_in_a_graph_and_repeats_bitwise():
     c = Case([70, 3, 0, 129], 136, 72, True, seed=9)
     outs = lambda: [torch.zeros(c.R, c.up, dtype=BF16, device=dev()), torch.zeros_like(c.w2),

@@ -102,6 +102,15 @@ def test_route_sigmoid_backward_refusals(L, bad):
     assert L.moe_route_sigmoid_backward(ctypes.byref(s), *a.values(), None) == N.MOE_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("bad", [dict(dl=None), dict(x=None), dict(w=ODD), dict(g=None), dict(dx=ODD), dict(dw=ODD),
+                                 dict(wgrad=3), dict(dx=None, dw=None), dict(ws=None), dict(bytes=100)])
+def test_gate_backward_refusals(L, bad):
+    s = shape()
+    a = dict(dl=A, x=A, w=A, g=A, dx=A, dw=A, wgrad=0, ws=WS, bytes=size(s))
+    a.update(bad)
+    assert L.moe_gate_backward(ctypes.byref(s), *a.values(), None) == N.MOE_ERR_INVALID_ARG
+
+
 UP_TRAIN = dict(x=A, offsets=A, w13=A, pre=A, h=A)
 DOWN = dict(dy=A, offsets=A, w2=A, pre=A, h=A, dpre=A, dw2=A, wgrad=0)
 UP = dict(dpre=A, offsets=A, x=A, w13=A, dx=A, dw13=A, wgrad=0)
