@@ -15,6 +15,11 @@
 // under the next tile's main loop.  The rows form's epilogue applies the
 // activation's derivative: dpre = act'(pre) * dh, from the saved pre-activations.
 //
+// A group's last, partial row tile of the rows form runs with the operands swapped
+// (C^T = W^T A^T): the pair's 256 weight columns on the MMA's M side, the tile's
+// rows, padded to 16, on its N side, so that a few rows cost a few rows of tensor
+// work -- under the power cap saved work is saved time.
+//
 // One launch does both forms of one projection (dh with dW2, dx with dW13): they
 // read the same rows and need nothing of each other, a launch less costs a small
 // layer 8 us less, and the short tiles of the weights form fill the last, partly
@@ -342,7 +347,88 @@ __device__ __forceinline__ void act_tile(const GParams& p, uint32_t tl, int m0, 
     }
 }
 
-struct Tile { int g, m0, n0, row0, mrows; };
+// The pre-activations a warp of a swapped tile will read, into L2.
+template <bool GLU>
+__device__ __forceinline__ void swapped_prefetch(const GParams& p, int rows, int row0, int n0, int first, int lane) {
+    if (n0 >= p.N) return;
+    for (int r = first * 32 + lane; r < rows; r += 32 * (EPI_WARPS / 4)) {
+        const __nv_bfloat16* src = p.pre + (size_t)(row0 + r) * p.ldo + n0;
+        asm volatile("prefetch.global.L2 [%0];" :: "l"(src));
+        if (GLU) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + p.up_off));
+    }
+}
+
+// A swapped tile: lane = output column n0 + lane, accumulator column = row.  The two
+// warps of a lane quarter take its 32-row chunks in turn, through a slot of [32 rows x
+// 32 columns] (SwiGLU: gate, then up), pre-activations fetched into it first.
+template <int ACT, typename F>
+__device__ __forceinline__ void swapped_tile(const GParams& p, uint32_t tl, int rows, int row0, int n0, int first,
+                                             uint8_t* s, int lane, F&& release) {
+    constexpr int STEP = EPI_WARPS / 4;
+    const int u = lane & 3, col = n0 + u * 8;
+    __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(s) + lane;
+    int last = (rows - 1) / 32;                                   // this warp's last chunk
+    last -= (last - first) & (STEP - 1);
+    if (first > last) release();
+#pragma unroll 1
+    for (int c = first; c * 32 < rows; c += STEP) {
+        const int left = rows - c * 32;
+        const size_t base = (size_t)(row0 + c * 32) * p.ldo + col;
+        if (ACT != kPlain) {
+            if (col < p.N) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = i * 8 + (lane >> 2);
+                    if (r < left) {
+                        const __nv_bfloat16* src = p.pre + base + (size_t)r * p.ldo;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(s + r * 64 + u * 16)), "l"(src) : "memory");
+                        if (ACT == kSwiGLU)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                         :: "r"(smem_u32(s + 2048 + r * 64 + u * 16)), "l"(src + p.up_off) : "memory");
+                    }
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        uint32_t v[32];
+        tmem_ld_32cols(tl + c * 32, v);
+        if (ACT != kPlain) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        tmem_ld_wait();
+        if (c == last) release();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            float f = __uint_as_float(v[j]);
+            if (ACT == kSwiGLU) {
+                float dg, du;
+                swiglu_grad(f, __bfloat162float(mine[j * 32]), __bfloat162float(mine[1024 + j * 32]), dg, du);
+                mine[1024 + j * 32] = __float2bfloat16_rn(du);
+                f = dg;
+            } else if (ACT == kReLU2) {
+                f *= 2.0f * relu(__bfloat162float(mine[j * 32]));
+            }
+            mine[j * 32] = __float2bfloat16_rn(f);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2);
+            if (r < left && col < p.N) {
+                __nv_bfloat16* o = p.out + base + (size_t)r * p.ldo;
+                *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(s + r * 64 + u * 16);
+                if (ACT == kSwiGLU)
+                    *reinterpret_cast<uint4*>(o + p.up_off) = *reinterpret_cast<const uint4*>(s + 2048 + r * 64 + u * 16);
+            }
+        }
+        __syncwarp();
+    }
+}
+
+struct Tile {
+    int g, m0, n0, row0, mrows;
+    __device__ __forceinline__ bool partial() const { return mrows - m0 < TM; }          // rows form
+    __device__ __forceinline__ int padded() const { return (mrows - m0 + 15) & ~15; }
+};
 
 // Tile `local` of a group of mtiles row tiles: bands of kBand column tiles, row
 // tiles first inside a band, so the tiles in flight share their operands in L2.
@@ -525,7 +611,9 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 const bool weights = tile >= nrows;
                 const Tile t = weights ? weights_tile(tile - nrows, rstart, rcount, wtm, wtn)
                                        : rows_tile(tile, prefix, rstart, rcount, p.groups);
-                const int a0 = t.m0 + (int)rank * HALF;          // A's row (rows form) or column
+                const bool swap = !weights && t.partial();
+                // this CTA's rows (rows form) or columns of A: 128, or half of the padded rows
+                const int a0 = t.m0 + (int)rank * (swap ? t.padded() / 2 : HALF);
                 const int b0 = t.n0 + (int)rank * HALF;
                 // one loop for each form: a step has 512 cycles, and one thread issues it
                 auto load = [&](auto form) {
@@ -554,10 +642,12 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                                 tma_load_2d_pair(sb + BOX_BYTES, &tmWB, full_leader, b0 + 64, y);
                             }
                         } else {
+                            // swapped: weights in the MMA's A slot, rows in its B slot
+                            const uint32_t s_rows = swap ? sb : sa, s_w = swap ? sa : sb;
                             if (rank == 0) mbar_arrive_expect_tx(full_local, 2 * STAGE_BYTES);
-                            tma_load_2d_pair(sa, &tmA, full_leader, i * BK, t.row0 + a0);
-                            tma_load_3d_pair(sb, &tmB, full_leader, b0, i * BK, t.g);
-                            tma_load_3d_pair(sb + BOX_BYTES, &tmB, full_leader, b0 + 64, i * BK, t.g);
+                            tma_load_2d_pair(s_rows, &tmA, full_leader, i * BK, t.row0 + a0);
+                            tma_load_3d_pair(s_w, &tmB, full_leader, b0, i * BK, t.g);
+                            tma_load_3d_pair(s_w + BOX_BYTES, &tmB, full_leader, b0 + 64, i * BK, t.g);
                         }
                         ++armed;
                         if (++stage == stages) { stage = 0; ph ^= 1u; }
@@ -584,33 +674,36 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             bool ok = true;
             for (int tile; ok && (tile = walk.next()) >= 0;) {
                 const bool weights = tile >= nrows;
-                const int mrows = weights ? rcount[(tile - nrows) / (wtm * wtn)] : 1;
-                if (mrows == 0) continue;
+                Tile t{};
+                if (weights) t.mrows = rcount[(tile - nrows) / (wtm * wtn)];
+                else t = rows_tile(tile, prefix, rstart, rcount, p.groups);
+                if (t.mrows == 0) continue;
                 if (!mbar_wait_cluster(smem_u32(&ctl->tempty[acc]), aph ^ 1u, abort)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(acc * TN);
-                auto multiply = [&](auto form) {
-                    constexpr bool kW = decltype(form)::value;
-                    constexpr uint32_t idesc = idesc_bf16_f32(TM, TN) | kMajorB | (kW ? kMajorA : 0u);
-                    constexpr uint64_t astep = kW ? kMnStep : kKStep;
-                    const int nk = kW ? (mrows + BK - 1) / BK : nk_rows;
+                // A and B: MN-major (boxes of reduction rows) or K-major
+                auto multiply = [&](auto a_mn, auto b_mn, uint32_t idesc) {
+                    constexpr bool kAmn = decltype(a_mn)::value, kBmn = decltype(b_mn)::value, kW = kAmn && kBmn;
+                    const int nk = kW ? (t.mrows + BK - 1) / BK : nk_rows;
                     for (int i = 0; i < nk; ++i) {
                         if (!mbar_wait_bounded(smem_u32(&ctl->full[stage]), ph, abort)) { ok = false; break; }
                         tc_fence_after();
-                        const uint32_t sa = smem_base + stage * STAGE_BYTES;
-                        const uint64_t ad = kW ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
-                        const uint64_t bd = sdesc_mn_sw128(sa + OP_BYTES);
+                        const uint32_t sa = smem_base + stage * STAGE_BYTES, sb = sa + OP_BYTES;
+                        const uint64_t ad = kAmn ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
+                        const uint64_t bd = kBmn ? sdesc_mn_sw128(sb) : sdesc_k_sw128(sb);
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
-                            if (!kW || i * BK + kk * 16 < mrows)          // slices that hold rows
-                                tc_mma_bf16_pair(d, ad + (uint64_t)kk * astep, bd + (uint64_t)kk * kMnStep, idesc,
+                            if (!kW || i * BK + kk * 16 < t.mrows)        // slices that hold rows
+                                tc_mma_bf16_pair(d, ad + (uint64_t)kk * (kAmn ? kMnStep : kKStep),
+                                                 bd + (uint64_t)kk * (kBmn ? kMnStep : kKStep), idesc,
                                                  (i > 0 || kk > 0) ? 1u : 0u);
                         tc_commit_pair_mc(smem_u32(&ctl->empty[stage]), (uint16_t)3);
                         if (++stage == stages) { stage = 0; ph ^= 1u; }
                     }
                 };
-                if (weights) multiply(std::true_type{});
-                else multiply(std::false_type{});
+                if (weights) multiply(std::true_type{}, std::true_type{}, idesc_bf16_f32(TM, TN) | kMajorA | kMajorB);
+                else if (t.partial()) multiply(std::true_type{}, std::false_type{}, idesc_bf16_f32(TM, t.padded()) | kMajorA);
+                else multiply(std::false_type{}, std::true_type{}, idesc_bf16_f32(TM, TN) | kMajorB);
                 if (!ok) break;
                 tc_commit_pair_mc(smem_u32(&ctl->tfull[acc]), (uint16_t)3);
                 acc ^= 1;
@@ -640,7 +733,14 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const int rows = (weights ? p.wM : t.mrows) - m0;            // of its 32 rows, those below the bound
             const int n0 = t.n0 + c0;
             const bool empty = weights && t.mrows == 0;                  // zeros, no accumulator
-            if (ACT != kPlain && !weights) act_prefetch<ACT == kSwiGLU>(p, m0, rows, t.row0, n0, epi, lane);
+            const bool swap = !weights && t.partial();
+            if (ACT != kPlain && !weights) {
+                if (!swap)
+                    act_prefetch<ACT == kSwiGLU>(p, m0, rows, t.row0, n0, epi, lane);
+                else
+                    swapped_prefetch<ACT == kSwiGLU>(p, t.mrows - t.m0, t.row0 + t.m0, t.n0 + (int)rank * HALF + q * 32,
+                                                     (warp - 2) / 4, lane);
+            }
             if (!empty) {
                 if (!mbar_wait_bounded(smem_u32(&ctl->tfull[acc]), aph, abort)) {
                     if (lane == 0) {
@@ -657,7 +757,10 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 __syncwarp();
                 if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&ctl->tempty[acc]), 0));
             };
-            if (weights && p.wmode != MOE_WGRAD_BF16) {
+            if (swap) {
+                swapped_tile<ACT>(p, tl - c0, t.mrows - t.m0, t.row0 + t.m0, t.n0 + (int)rank * HALF + q * 32,
+                                  (warp - 2) / 4, epi, lane, release);
+            } else if (weights && p.wmode != MOE_WGRAD_BF16) {
                 if (!(empty && p.wmode == MOE_WGRAD_F32_ADD))
                     f32_tile(p, tl, empty, rows, n0,
                              static_cast<float*>(p.wout) + ((size_t)t.g * p.wM + m0) * p.wN, epi, lane, release);
