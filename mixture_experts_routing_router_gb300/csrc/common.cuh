@@ -580,9 +580,10 @@ struct LayerNormProblem {
     float* dbeta;
     float* scratch;                  // [layernorm_parts(rows)][2][hidden]
 };
-// Partial sums of the weight's gradient: at most two blocks per SM of a GB300.
+// Partial sums of the weight's gradient: one per block, at most two blocks per SM of
+// a GB300, and the eight that rows of odd width need.
 constexpr int kLayerNormParts = 304;
-inline int layernorm_parts(long long rows) { return rows < kLayerNormParts ? (rows < 1 ? 1 : (int)rows) : kLayerNormParts; }
+inline int layernorm_parts(long long rows) { return rows < kLayerNormParts ? (rows < 8 ? 8 : (int)rows) : kLayerNormParts; }
 cudaError_t launch_layernorm(const LayerNormProblem& p, cudaStream_t st);
 cudaError_t launch_layernorm_backward(const LayerNormProblem& p, cudaStream_t st);
 

@@ -137,11 +137,14 @@ layernorm_dw_partial_kernel(long long rows, int H, const T* __restrict__ dy, con
 }
 
 // ---- rows held by TPR threads ---------------------------------------------------
-// One access of a thread: 16 bytes where rows are 16-byte aligned (hidden a
-// multiple of 8 BF16 / 4 FP32), else one element.
-template <typename T, int VN> struct Raw { using type = uint4; };
-template <> struct Raw<__nv_bfloat16, 1> { using type = unsigned short; };
-template <> struct Raw<float, 1> { using type = float; };
+// One access of a thread is 16 bytes: VN elements.  When hidden is no multiple of VN
+// the rows start at offsets inside such a chunk that repeat every VN rows at most.
+// A row group then only takes rows of one offset (the number of groups is a multiple
+// of VN), so a thread still has the same columns in every row; its chunks begin at
+// the chunk boundary before the row, and the first and last one, which the row shares
+// with its neighbours, are written element by element.  ([16384, 7167] BF16 forward:
+// 153 us, backward 225; single elements throughout: 255 and 629.)
+template <typename T> constexpr int kVN = 16 / (int)sizeof(T);
 
 __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -154,8 +157,6 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
 __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
     f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
 }
-__device__ __forceinline__ void unpack(unsigned short v, float (&f)[1]) { f[0] = __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ void unpack(float v, float (&f)[1]) { f[0] = v; }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&b);
@@ -166,49 +167,70 @@ __device__ __forceinline__ void store(uint4* p, const float (&f)[8]) {
 __device__ __forceinline__ void store(uint4* p, const float (&f)[4]) {
     __stcs(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
 }
-__device__ __forceinline__ void store(unsigned short* p, const float (&f)[1]) {
-    *p = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+// The VN elements from element c of row `out`, those inside [0, H) of a shared chunk.
+template <int VN, typename T>
+__device__ __forceinline__ void store_chunk(T* out, int c, int H, bool whole, const float (&f)[VN]) {
+    if (whole) {
+        store(reinterpret_cast<uint4*>(out + c), f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+            if (c + e >= 0 && c + e < H) out[c + e] = from_f32<T>(f[e]);
+    }
 }
-__device__ __forceinline__ void store(float* p, const float (&f)[1]) { *p = f[0]; }
 
-// VN weights from column c (a multiple of VN); every row of an SM reads them
-// again, from L1.
+// The VN weights from column c, zeros outside [0, H).
 template <int VN>
-__device__ __forceinline__ void load_weight(const void* w, bool bf16, int c, float (&f)[VN]) {
-    if (bf16) {
+__device__ __forceinline__ void load_weight(const void* w, bool bf16, int c, int H, bool whole, float (&f)[VN]) {
+    if (!whole) {
+#pragma unroll
+        for (int e = 0; e < VN; ++e) {
+            const int i = c + e;
+            f[e] = i < 0 || i >= H ? 0.f
+                   : bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]) : static_cast<const float*>(w)[i];
+        }
+    } else if ((c & (VN - 1)) != 0) {          // whole, but off the weights' own chunks
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+            f[e] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c + e]) : static_cast<const float*>(w)[c + e];
+    } else if (bf16) {
         const unsigned short* p = static_cast<const unsigned short*>(w) + c;
         if constexpr (VN == 8) {
             unpack(__ldg(reinterpret_cast<const uint4*>(p)), f);
-        } else if constexpr (VN == 4) {
+        } else {
             const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
             f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
             f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
-        } else {
-            f[0] = __uint_as_float((uint32_t)__ldg(p) << 16);
         }
     } else {
         const float* p = static_cast<const float*>(w) + c;
-        if constexpr (VN == 1) {
-            f[0] = __ldg(p);
-        } else {
 #pragma unroll
-            for (int i = 0; i < VN / 4; ++i) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-                f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
-            }
+        for (int i = 0; i < VN / 4; ++i) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+            f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
         }
     }
 }
 
-// Copy one access into this thread's shared-memory slot: asynchronously (16 or 4
-// bytes), or, for single BF16 elements, at once.
-__device__ __forceinline__ void copy_async(uint4* dst, const uint4* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
+// Copy the chunk from element c of a row into this thread's slot.  A chunk shared with
+// a neighbouring row is copied whole too (clear() drops what is not the row's); only
+// one that reaches past the tensor's end (`inside` false) goes element by element.
+template <typename T>
+__device__ __forceinline__ void fetch_chunk(uint4* slot, const T* row, int c, int H, bool inside) {
+    if (inside) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(slot)), "l"(row + c) : "memory");
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVN<T>; ++e)
+            if (c + e >= 0 && c + e < H) reinterpret_cast<T*>(slot)[e] = row[c + e];
+    }
 }
-__device__ __forceinline__ void copy_async(float* dst, const float* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
+template <int VN>
+__device__ __forceinline__ void clear(float (&f)[VN], int c, int H) {
+#pragma unroll
+    for (int e = 0; e < VN; ++e)
+        if (c + e < 0 || c + e >= H) f[e] = 0.f;
 }
-__device__ __forceinline__ void copy_async(unsigned short* dst, const unsigned short* src) { *dst = *src; }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
@@ -251,31 +273,49 @@ template <typename T> constexpr int stages_of(int arrays, int cols) {
 }
 constexpr int kFwdCols = 32, kBwdCols = 16;        // columns a thread (backward above 8192 columns: 32)
 
-template <typename T, int VN, int TPR>
+// What every thread of a row group knows about its columns: element `at(i)` of the
+// row begins its i-th chunk; `has` it any element, are they all the row's (`whole`).
+// ODD: the row is not a whole number of chunks.
+template <typename T, int TPR, bool ODD>
+struct Columns {
+    static constexpr int VN = kVN<T>;
+    int H, lane, shift;
+    __device__ __forceinline__ Columns(int H_, int lane_, long long row) : H(H_), lane(lane_), shift(0) {
+        if (ODD) shift = (int)((unsigned long long)row * (unsigned)H_ % VN);
+    }
+    __device__ __forceinline__ int at(int i) const { return (lane + i * TPR) * VN - shift; }
+    __device__ __forceinline__ bool has(int i) const { return at(i) < H; }
+    __device__ __forceinline__ bool whole(int i) const { return !ODD || (at(i) >= 0 && at(i) + VN <= H); }
+    __device__ __forceinline__ bool inside(int i, long long row, long long rows) const {
+        return !ODD || at(i) + VN <= (rows - row) * H;
+    }
+};
+
+template <typename T, int TPR, bool ODD>
 __global__ void __launch_bounds__(NT, 1)
 layernorm_rows_kernel(long long rows, int H, const T* x, const void* __restrict__ gamma,
                       const void* __restrict__ beta, bool wbf16, float eps, T* y, float* __restrict__ mean,
                       float* __restrict__ rstd) {
-    using R = typename Raw<T, VN>::type;
-    constexpr int RPB = NT / TPR, V = kFwdCols / VN, S = stages_of<T>(1, kFwdCols);
+    constexpr int VN = kVN<T>, RPB = NT / TPR, V = kFwdCols / VN, S = stages_of<T>(1, kFwdCols);
     static_assert(S >= 2, "stages");
     extern __shared__ __align__(16) uint8_t smem_ln[];
-    R* slots = reinterpret_cast<R*>(smem_ln);                     // [stage][V][NT]
+    uint4* slots = reinterpret_cast<uint4*>(smem_ln);             // [stage][V][NT]
     __shared__ float red[2 * NT / 32];
     const int tid = threadIdx.x, group = tid / TPR, lane = tid % TPR;
-    const int HV = H / VN;
-    const long long step = (long long)gridDim.x * RPB;
+    const long long first = (long long)blockIdx.x * RPB + group, step = (long long)gridDim.x * RPB;
+    const Columns<T, TPR, ODD> col(H, lane, first);
     int flip = 0;
     const float inv = 1.0f / (float)H;
     pdl_wait();
     pdl_trigger();
-    long long next = (long long)blockIdx.x * RPB + group;
+    long long next = first;
     auto fetch = [&](int stage) {
         if (next < rows) {
-            const R* xr = reinterpret_cast<const R*>(x + (size_t)next * H);
+            const T* xr = x + (size_t)next * H;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (lane + i * TPR < HV) copy_async(slots + (stage * V + i) * NT + tid, xr + lane + i * TPR);
+                if (col.has(i))
+                    fetch_chunk(slots + (stage * V + i) * NT + tid, xr, col.at(i), H, col.inside(i, next, rows));
         }
         copy_commit();
         next += step;
@@ -285,20 +325,21 @@ layernorm_rows_kernel(long long rows, int H, const T* x, const void* __restrict_
     float g[V][VN], b[V][VN];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        if (lane + i * TPR < HV) {
-            load_weight<VN>(gamma, wbf16, (lane + i * TPR) * VN, g[i]);
-            load_weight<VN>(beta, wbf16, (lane + i * TPR) * VN, b[i]);
+        if (col.has(i)) {
+            load_weight<VN>(gamma, wbf16, col.at(i), H, col.whole(i), g[i]);
+            load_weight<VN>(beta, wbf16, col.at(i), H, col.whole(i), b[i]);
         }
     int stage = 0;
-    for (long long r = (long long)blockIdx.x * RPB + group; r < rows; r += step) {
+    for (long long r = first; r < rows; r += step) {
         fetch(stage == 0 ? S - 1 : stage - 1);
         copy_wait<S - 1>();
         float v[V][VN];
         float s[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (lane + i * TPR < HV) {
+            if (col.has(i)) {
                 unpack(slots[(stage * V + i) * NT + tid], v[i]);
+                if (!col.whole(i)) clear(v[i], col.at(i), H);
 #pragma unroll
                 for (int e = 0; e < VN; ++e) s[0] += v[i][e];
             }
@@ -307,22 +348,22 @@ layernorm_rows_kernel(long long rows, int H, const T* x, const void* __restrict_
         float q[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (lane + i * TPR < HV) {
+            if (col.has(i)) {
 #pragma unroll
-                for (int e = 0; e < VN; ++e) {
-                    v[i][e] -= mu;
-                    q[0] = fmaf(v[i][e], v[i][e], q[0]);
-                }
+                for (int e = 0; e < VN; ++e) v[i][e] -= mu;
+                if (!col.whole(i)) clear(v[i], col.at(i), H);
+#pragma unroll
+                for (int e = 0; e < VN; ++e) q[0] = fmaf(v[i][e], v[i][e], q[0]);
             }
         row_sum<TPR>(q, red, group, flip);
         const float rs = 1.0f / sqrtf(q[0] * inv + eps);
-        R* yr = reinterpret_cast<R*>(y + (size_t)r * H);
+        T* yr = y + (size_t)r * H;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (lane + i * TPR < HV) {
+            if (col.has(i)) {
 #pragma unroll
                 for (int e = 0; e < VN; ++e) v[i][e] = fmaf(v[i][e] * rs, g[i][e], b[i][e]);
-                store(yr + lane + i * TPR, v[i]);
+                store_chunk<VN>(yr, col.at(i), H, col.whole(i), v[i]);
             }
         if (lane == 0) {
             if (mean) mean[r] = mu;
@@ -334,21 +375,20 @@ layernorm_rows_kernel(long long rows, int H, const T* x, const void* __restrict_
 
 // 16 columns a thread: the row's x and dy and the weights stay in registers
 // between the two passes over it; 32: they are read again (slots, L1).
-template <typename T, int VN, int TPR, int COLS>
+template <typename T, int TPR, int COLS, bool ODD>
 __global__ void __launch_bounds__(NT, 1)
 layernorm_grad_rows_kernel(long long rows, int H, const T* dy, const T* x, const void* __restrict__ gamma, bool wbf16,
                            const float* __restrict__ mean, const float* __restrict__ rstd, const T* dres, T* dx,
                            float* __restrict__ part) {
-    using R = typename Raw<T, VN>::type;
-    constexpr int RPB = NT / TPR, V = COLS / VN, S = stages_of<T>(3, COLS);
+    constexpr int VN = kVN<T>, RPB = NT / TPR, V = COLS / VN, S = stages_of<T>(3, COLS);
     constexpr bool kKeep = COLS == 16;
     static_assert(S >= 2, "stages");
     extern __shared__ __align__(16) uint8_t smem_ln[];
-    R* slots = reinterpret_cast<R*>(smem_ln);                     // [stage][x, dy, dres][V][NT]
+    uint4* slots = reinterpret_cast<uint4*>(smem_ln);             // [stage][x, dy, dres][V][NT]
     __shared__ float red[2 * 2 * NT / 32];
     const int tid = threadIdx.x, group = tid / TPR, lane = tid % TPR;
-    const int HV = H / VN;
-    const long long step = (long long)gridDim.x * RPB;
+    const long long first = (long long)blockIdx.x * RPB + group, step = (long long)gridDim.x * RPB;
+    const Columns<T, TPR, ODD> col(H, lane, first);
     int flip = 0;
     const float inv = 1.0f / (float)H;
     float dg[V][VN], db[V][VN], gk[kKeep ? V : 1][VN];
@@ -358,19 +398,19 @@ layernorm_grad_rows_kernel(long long rows, int H, const T* dy, const T* x, const
         for (int e = 0; e < VN; ++e) dg[i][e] = db[i][e] = 0.f;
     pdl_wait();
     pdl_trigger();
-    long long next = (long long)blockIdx.x * RPB + group;
+    long long next = first;
     auto fetch = [&](int stage) {
         if (next < rows) {
             const size_t o = (size_t)next * H;
-            const R* src[3] = {reinterpret_cast<const R*>(x + o), reinterpret_cast<const R*>(dy + o),
-                               dres ? reinterpret_cast<const R*>(dres + o) : nullptr};
+            const T* src[3] = {x + o, dy + o, dres ? dres + o : nullptr};
 #pragma unroll
             for (int a = 0; a < 3; ++a) {
                 if (a == 2 && !dres) break;
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (lane + i * TPR < HV)
-                        copy_async(slots + ((stage * 3 + a) * V + i) * NT + tid, src[a] + lane + i * TPR);
+                    if (col.has(i))
+                        fetch_chunk(slots + ((stage * 3 + a) * V + i) * NT + tid, src[a], col.at(i), H,
+                                    col.inside(i, next, rows));
             }
         }
         copy_commit();
@@ -378,7 +418,6 @@ layernorm_grad_rows_kernel(long long rows, int H, const T* dy, const T* x, const
     };
 #pragma unroll 1
     for (int s = 0; s < S - 1; ++s) fetch(s);
-    const long long first = (long long)blockIdx.x * RPB + group;
     float mu_n = 0.f, rs_n = 0.f;                                 // of the next row
     if (first < rows) {
         mu_n = mean[first];
@@ -387,7 +426,7 @@ layernorm_grad_rows_kernel(long long rows, int H, const T* dy, const T* x, const
     if constexpr (kKeep) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (lane + i * TPR < HV) load_weight<VN>(gamma, wbf16, (lane + i * TPR) * VN, gk[i]);
+            if (col.has(i)) load_weight<VN>(gamma, wbf16, col.at(i), H, col.whole(i), gk[i]);
     }
     int stage = 0;
     for (long long r = first; r < rows; r += step) {
@@ -398,20 +437,24 @@ layernorm_grad_rows_kernel(long long rows, int H, const T* dy, const T* x, const
         }
         fetch(stage == 0 ? S - 1 : stage - 1);
         copy_wait<S - 1>();
-        const R* sx = slots + (size_t)(stage * 3) * V * NT + tid;
-        const R* sy = sx + V * NT;
-        const R* sr = sy + V * NT;
-        R rx[V], ry[V];
+        const uint4* sx = slots + (size_t)(stage * 3) * V * NT + tid;
+        const uint4* sy = sx + V * NT;
+        const uint4* sr = sy + V * NT;
+        uint4 rx[V], ry[V];
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (lane + i * TPR < HV) {
+            if (col.has(i)) {
                 float xv[VN], dv[VN], g[VN];
                 rx[i] = sx[i * NT];
                 ry[i] = sy[i * NT];
                 unpack(rx[i], xv);
                 unpack(ry[i], dv);
-                if constexpr (!kKeep) load_weight<VN>(gamma, wbf16, (lane + i * TPR) * VN, g);
+                if (!col.whole(i)) {
+                    clear(xv, col.at(i), H);
+                    clear(dv, col.at(i), H);
+                }
+                if constexpr (!kKeep) load_weight<VN>(gamma, wbf16, col.at(i), H, col.whole(i), g);
 #pragma unroll
                 for (int e = 0; e < VN; ++e) {
                     const float xh = (xv[e] - mu) * rs, a = dv[e] * (kKeep ? gk[kKeep ? i : 0][e] : g[e]);
@@ -423,14 +466,14 @@ layernorm_grad_rows_kernel(long long rows, int H, const T* dy, const T* x, const
             }
         row_sum<TPR>(s, red, group, flip);
         const float ma = s[0] * inv, mb = s[1] * inv;
-        R* out = reinterpret_cast<R*>(dx + (size_t)r * H);
+        T* out = dx + (size_t)r * H;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (lane + i * TPR < HV) {
+            if (col.has(i)) {
                 float xv[VN], dv[VN], g[VN];
                 unpack(kKeep ? rx[i] : sx[i * NT], xv);
                 unpack(kKeep ? ry[i] : sy[i * NT], dv);
-                if constexpr (!kKeep) load_weight<VN>(gamma, wbf16, (lane + i * TPR) * VN, g);
+                if constexpr (!kKeep) load_weight<VN>(gamma, wbf16, col.at(i), H, col.whole(i), g);
 #pragma unroll
                 for (int e = 0; e < VN; ++e)
                     dv[e] = (dv[e] * (kKeep ? gk[kKeep ? i : 0][e] : g[e]) - ma - (xv[e] - mu) * rs * mb) * rs;
@@ -439,7 +482,7 @@ layernorm_grad_rows_kernel(long long rows, int H, const T* dy, const T* x, const
 #pragma unroll
                     for (int e = 0; e < VN; ++e) dv[e] += xv[e];
                 }
-                store(out + lane + i * TPR, dv);
+                store_chunk<VN>(out, col.at(i), H, col.whole(i), dv);
             }
         stage = stage == S - 1 ? 0 : stage + 1;
     }
@@ -455,8 +498,8 @@ layernorm_grad_rows_kernel(long long rows, int H, const T* dy, const T* x, const
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int e = 0; e < VN; ++e) {
-            const int c = (lane + i * TPR) * VN + e;
-            if (c < H) {
+            const int c = col.at(i) + e;
+            if (c >= 0 && c < H) {
                 acc[c] = dg[i][e];
                 acc[H + c] = db[i][e];
             }
@@ -552,21 +595,28 @@ cudaError_t allow_smem(K kernel, size_t bytes, std::once_flag& once, cudaError_t
     return err;
 }
 
-template <typename T, int VN, int TPR>
+// Blocks of `rpb` row groups: a block for each SM at most; for odd rows the number of
+// groups is a multiple of vn.
+unsigned blocks_of(long long rows, int rpb, bool odd, int vn) {
+    long long blocks = (rows + rpb - 1) / rpb;
+    if (blocks > device_sm_count()) blocks = device_sm_count();
+    const int unit = odd && rpb < vn ? vn / rpb : 1;
+    blocks = blocks < device_sm_count() / unit * unit ? (blocks + unit - 1) / unit * unit : blocks / unit * unit;
+    return (unsigned)(blocks < unit ? unit : blocks);
+}
+
+template <typename T, int TPR, bool ODD>
 cudaError_t forward_rows(const LayerNormProblem& p, cudaStream_t st) {
-    constexpr int RPB = NT / TPR;
     constexpr size_t smem = (size_t)stages_of<T>(1, kFwdCols) * kFwdCols * sizeof(T) * NT;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
-    if (allow_smem(layernorm_rows_kernel<T, VN, TPR>, smem, once, err) != cudaSuccess) return err;
-    long long blocks = (p.rows + RPB - 1) / RPB;
-    if (blocks > device_sm_count()) blocks = device_sm_count();
-    return launch_kernel(layernorm_rows_kernel<T, VN, TPR>, dim3((unsigned)blocks), dim3(NT), smem, st, 1, kUsePdl,
-                         p.rows, p.hidden, static_cast<const T*>(p.x), p.gamma, p.beta, p.wtype == MOE_TYPE_BF16,
-                         p.eps, static_cast<T*>(p.y), p.mean, p.rstd);
+    if (allow_smem(layernorm_rows_kernel<T, TPR, ODD>, smem, once, err) != cudaSuccess) return err;
+    return launch_kernel(layernorm_rows_kernel<T, TPR, ODD>, dim3(blocks_of(p.rows, NT / TPR, ODD, kVN<T>)), dim3(NT),
+                         smem, st, 1, kUsePdl, p.rows, p.hidden, static_cast<const T*>(p.x), p.gamma, p.beta,
+                         p.wtype == MOE_TYPE_BF16, p.eps, static_cast<T*>(p.y), p.mean, p.rstd);
 }
 
-template <typename T, int VN, int TPR, int COLS>
+template <typename T, int TPR, int COLS, bool ODD>
 cudaError_t backward_rows(const LayerNormProblem& p, cudaStream_t st) {
     constexpr int RPB = NT / TPR;
     constexpr size_t smem = (size_t)stages_of<T>(3, COLS) * 3 * COLS * sizeof(T) * NT;
@@ -574,51 +624,50 @@ cudaError_t backward_rows(const LayerNormProblem& p, cudaStream_t st) {
     static_assert(RPB == 1 || smem >= (size_t)NT * 2 * COLS * sizeof(float), "partial sums");
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
-    if (allow_smem(layernorm_grad_rows_kernel<T, VN, TPR, COLS>, smem, once, err) != cudaSuccess) return err;
-    long long blocks = (p.rows + RPB - 1) / RPB;
-    const long long cap = device_sm_count() < kLayerNormParts ? device_sm_count() : kLayerNormParts;
-    if (blocks > cap) blocks = cap;
+    if (allow_smem(layernorm_grad_rows_kernel<T, TPR, COLS, ODD>, smem, once, err) != cudaSuccess) return err;
+    const unsigned blocks = blocks_of(p.rows, RPB, ODD, kVN<T>);
+    if ((int)blocks > layernorm_parts(p.rows)) return cudaErrorInvalidConfiguration;      // the scratch is sized by it
     const cudaError_t e =
-        launch_kernel(layernorm_grad_rows_kernel<T, VN, TPR, COLS>, dim3((unsigned)blocks), dim3(NT), smem, st, 1,
-                      kUsePdl, p.rows, p.hidden, static_cast<const T*>(p.dy), static_cast<const T*>(p.x), p.gamma,
+        launch_kernel(layernorm_grad_rows_kernel<T, TPR, COLS, ODD>, dim3(blocks), dim3(NT), smem, st, 1, kUsePdl,
+                      p.rows, p.hidden, static_cast<const T*>(p.dy), static_cast<const T*>(p.x), p.gamma,
                       p.wtype == MOE_TYPE_BF16, static_cast<const float*>(p.mean), static_cast<const float*>(p.rstd),
                       static_cast<const T*>(p.dres), static_cast<T*>(p.dx), p.scratch);
     return e != cudaSuccess ? e : finish_weights(p, (int)blocks, st);
 }
 
-// The fewest threads whose columns cover the row (whole warps share a row).
-template <typename T, int VN>
+// The fewest threads whose columns cover the row, wherever it starts in a chunk
+// (whole warps share a row).
+template <typename T, bool ODD>
 bool forward_by_width(const LayerNormProblem& p, cudaStream_t st, cudaError_t* e) {
-    const int need = (p.hidden + kFwdCols - 1) / kFwdCols;
-    if (need <= 32) *e = forward_rows<T, VN, 32>(p, st);
-    else if (need <= 64) *e = forward_rows<T, VN, 64>(p, st);
-    else if (need <= 128) *e = forward_rows<T, VN, 128>(p, st);
-    else if (need <= 256) *e = forward_rows<T, VN, 256>(p, st);
-    else if (need <= 512) *e = forward_rows<T, VN, 512>(p, st);
+    const int need = (p.hidden + (ODD ? kVN<T> - 1 : 0) + kFwdCols - 1) / kFwdCols;
+    if (need <= 32) *e = forward_rows<T, 32, ODD>(p, st);
+    else if (need <= 64) *e = forward_rows<T, 64, ODD>(p, st);
+    else if (need <= 128) *e = forward_rows<T, 128, ODD>(p, st);
+    else if (need <= 256) *e = forward_rows<T, 256, ODD>(p, st);
+    else if (need <= 512) *e = forward_rows<T, 512, ODD>(p, st);
     else return false;
     return true;
 }
 
-template <typename T, int VN>
+template <typename T, bool ODD>
 bool backward_by_width(const LayerNormProblem& p, cudaStream_t st, cudaError_t* e) {
-    const int need = (p.hidden + kBwdCols - 1) / kBwdCols;
-    if (need <= 32) *e = backward_rows<T, VN, 32, kBwdCols>(p, st);
-    else if (need <= 64) *e = backward_rows<T, VN, 64, kBwdCols>(p, st);
-    else if (need <= 128) *e = backward_rows<T, VN, 128, kBwdCols>(p, st);
-    else if (need <= 256) *e = backward_rows<T, VN, 256, kBwdCols>(p, st);
-    else if (need <= 512) *e = backward_rows<T, VN, 512, kBwdCols>(p, st);
-    else if (sizeof(T) == 2 && need <= 1024) *e = backward_rows<__nv_bfloat16, sizeof(T) == 2 ? VN : 8, 512, 32>(p, st);
+    const int need = (p.hidden + (ODD ? kVN<T> - 1 : 0) + kBwdCols - 1) / kBwdCols;
+    if (need <= 32) *e = backward_rows<T, 32, kBwdCols, ODD>(p, st);
+    else if (need <= 64) *e = backward_rows<T, 64, kBwdCols, ODD>(p, st);
+    else if (need <= 128) *e = backward_rows<T, 128, kBwdCols, ODD>(p, st);
+    else if (need <= 256) *e = backward_rows<T, 256, kBwdCols, ODD>(p, st);
+    else if (need <= 512) *e = backward_rows<T, 512, kBwdCols, ODD>(p, st);
+    else if (sizeof(T) == 2 && need <= 1024) *e = backward_rows<__nv_bfloat16, 512, 32, ODD>(p, st);
     else return false;
     return true;
 }
 
 template <typename T>
 cudaError_t run(const LayerNormProblem& p, bool fwd, cudaStream_t st) {
-    constexpr int VN = 16 / (int)sizeof(T);
     cudaError_t e = cudaSuccess;
-    const bool vec = p.hidden % VN == 0;
-    if (fwd ? (vec ? forward_by_width<T, VN>(p, st, &e) : forward_by_width<T, 1>(p, st, &e))
-            : (vec ? backward_by_width<T, VN>(p, st, &e) : backward_by_width<T, 1>(p, st, &e)))
+    const bool odd = p.hidden % kVN<T> != 0;
+    if (fwd ? (odd ? forward_by_width<T, true>(p, st, &e) : forward_by_width<T, false>(p, st, &e))
+            : (odd ? backward_by_width<T, true>(p, st, &e) : backward_by_width<T, false>(p, st, &e)))
         return e;
     if (p.wtype == MOE_TYPE_BF16) return fwd ? forward_wide<T, __nv_bfloat16>(p, st) : backward_wide<T, __nv_bfloat16>(p, st);
     return fwd ? forward_wide<T, float>(p, st) : backward_wide<T, float>(p, st);
