@@ -460,7 +460,9 @@ MOE_API moe_status moe_expert_up_train(const moe_shape* shape, const uint16_t* x
  *        w2 and pre are then not read
  *   dw2  device [E, H, I] out, bf16 or f32, or NULL: h is then not read.  An expert
  *        without rows gets zeros (MOE_WGRAD_F32_ADD leaves it as it is).
- * Host error: MOE_ERR_INVALID_ARG when both outputs are NULL. */
+ * Host error: MOE_ERR_INVALID_ARG when both outputs are NULL.  Device error (here and
+ * in moe_expert_up_backward): MOE_ERR_INVALID_ROUTE when offsets decrease or leave
+ * [0, T*k]; no bucket has rows then. */
 MOE_API moe_status moe_expert_down_backward(const moe_shape* shape, const uint16_t* dy_perm, const int32_t* offsets,
                                             const uint16_t* w2, const uint16_t* pre, const uint16_t* h,
                                             uint16_t* dpre, void* dw2, int32_t wgrad, void* ws, size_t ws_bytes,

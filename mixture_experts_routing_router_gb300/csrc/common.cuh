@@ -581,9 +581,11 @@ struct LayerNormProblem {
     float* scratch;                  // [layernorm_parts(rows)][2][hidden]
 };
 // Partial sums of the weight's gradient: one per block, at most two blocks per SM of
-// a GB300, and the eight that rows of odd width need.
+// a GB300, a multiple of eight (rows of odd width take their blocks in such units).
 constexpr int kLayerNormParts = 304;
-inline int layernorm_parts(long long rows) { return rows < kLayerNormParts ? (rows < 8 ? 8 : (int)rows) : kLayerNormParts; }
+inline int layernorm_parts(long long rows) {
+    return rows >= kLayerNormParts ? kLayerNormParts : rows < 1 ? 8 : (int)((rows + 7) / 8 * 8);
+}
 cudaError_t launch_layernorm(const LayerNormProblem& p, cudaStream_t st);
 cudaError_t launch_layernorm_backward(const LayerNormProblem& p, cudaStream_t st);
 

@@ -62,7 +62,7 @@ constexpr int MAX_DYN_SMEM = 232448 - 1024;       // the opt-in limit less the k
 
 struct GParams {
     const int32_t* offsets;          // NULL: one group of all rows
-    int groups, a_rows;              // bucket bounds are clamped to [0, a_rows]
+    int groups, a_rows;              // the bounds lie in [0, a_rows]
     int stages;                      // of the shared-memory ring
     WsHeader* hdr;
     // rows form (N == 0: not asked for)
@@ -557,15 +557,20 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     tc_fence_after();
     pdl_wait();
     pdl_trigger();
-    // each bucket is clamped to [0, a_rows], so malformed offsets stay in bounds
+    // Bounds that decrease or leave [0, a_rows] are refused as a whole: with none of
+    // them the buckets are disjoint, so the tile count stays below the host's bound.
+    int bad = 0;
     for (int g = tid; g < p.groups; g += THREADS) {
-        int lo = p.offsets ? p.offsets[g] : 0, hi = p.offsets ? p.offsets[g + 1] : p.a_rows;
-        lo = lo < 0 ? 0 : (lo > p.a_rows ? p.a_rows : lo);
-        hi = hi < lo ? lo : (hi > p.a_rows ? p.a_rows : hi);
+        const int lo = p.offsets ? p.offsets[g] : 0, hi = p.offsets ? p.offsets[g + 1] : p.a_rows;
+        bad |= lo < 0 || hi < lo || hi > p.a_rows;
         rstart[g] = lo;
         rcount[g] = hi - lo;
     }
-    __syncthreads();
+    if (__syncthreads_or(bad)) {
+        for (int g = tid; g < p.groups; g += THREADS) rstart[g] = rcount[g] = 0;
+        if (tid == 0) raise_status(p.hdr, MOE_ERR_INVALID_ROUTE);
+        __syncthreads();
+    }
     {
         // exclusive scan of the rows form's tiles per group -> prefix[0..groups]
         const int n = p.groups;

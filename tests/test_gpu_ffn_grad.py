@@ -135,6 +135,23 @@ def test_float32_weight_gradients_and_accumulation(counts):
         assert torch.equal(dw.t[empty], old[empty])
 
 
+@pytest.mark.parametrize("bad", [[0, 60, 50, 100], [-1, 30, 60, 100], [0, 30, 60, 101], [0, 1 << 30, 60, 100],
+                                 [0, 30, -(1 << 31), 100]], ids=str)
+def test_bad_bucket_bounds_are_reported_and_move_nothing(bad):
+    c = Case([30, 30, 40], 72, 40, True, seed=11)
+    offsets = torch.tensor(bad, dtype=torch.int32, device=dev())
+    dpre, dx = Guarded((c.R, c.up), BF16), Guarded((c.R, c.H), BF16)
+    dw2, dw13 = Guarded((c.E, c.H, c.I), BF16), Guarded((c.E, c.up, c.H), BF16)
+    N.moe_expert_down_backward(c.shape, c.dy, offsets, c.w2, c.pre, c.h, dpre.t, dw2.t, c.ws)
+    assert N.moe_status_read(c.ws) == N.MOE_ERR_INVALID_ROUTE
+    N.moe_expert_up_backward(c.shape, c.dpre_in, offsets, c.x, c.w13, dx.t, dw13.t, c.ws)
+    assert N.moe_status_read(c.ws) == N.MOE_ERR_INVALID_ROUTE
+    for b in (dpre, dx, dw2, dw13):
+        assert b.intact()
+    for b in (dpre, dx):
+        assert torch.all(b.t.view(torch.uint8) == 0xA5)
+
+
 def test_a_bucket_of_nan_rows_stays_in_its_expert():
     counts = [40, 70, 1, 130, 17]
     c = Case(counts, 200, 136, True, seed=6)

@@ -76,6 +76,14 @@ def test_rows(rows, H):
     verify(x, gamma, beta, dy, None)
 
 
+@pytest.mark.parametrize("rows", [1, 7, 9, 20, 151, 153, 170])
+@pytest.mark.parametrize("H", [509, 1023, 2046, 4089, 7167, 8185, 9001, 16381])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_odd_widths_at_every_thread_count(rows, H, dtype):
+    x, gamma, beta, dy, dres = inputs(rows, H, dtype, F32, seed=rows + H)
+    verify(x, gamma, beta, dy, dres)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("wtype", [BF16, F32], ids=["wbf16", "wf32"])
 @pytest.mark.parametrize("H", [264, 7168, 515])
