@@ -317,9 +317,12 @@ def moe_timeout_site_read(ws, stream=None) -> int:
 
 
 # ---- training ---------------------------------------------------------------
+_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}
+
+
 def _type(t):
     try:
-        return {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}[t.dtype]
+        return _TYPES[t.dtype]
     except KeyError:
         raise ValueError(f"bfloat16 or float32 tensor expected, got {t.dtype}") from None
 
