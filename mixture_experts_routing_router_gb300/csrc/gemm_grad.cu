@@ -112,8 +112,8 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-// mbar_wait_bounded with the acquire at cluster scope: the fixer of the other
-// CTA of the pair arrives on the leader's barrier.
+// mbar_wait_bounded with the acquire at cluster scope: the other CTA of the pair
+// arrives on the leader's barrier (its fixer, its epilogue warps).
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort) {
     if (mbar_try_wait_cluster(bar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();

@@ -135,6 +135,25 @@ def test_float32_weight_gradients_and_accumulation(counts):
         assert torch.equal(dw.t[empty], old[empty])
 
 
+@pytest.mark.parametrize("glu", [True, False], ids=["swiglu", "relu2"])
+@pytest.mark.parametrize("rows", [40, 300])          # a swapped tile; a full one and a swapped one
+def test_saturated_pre_activations(rows, glu):
+    c = Case([rows], 72, 64, glu, seed=12)
+    pick = torch.tensor([-3e38, -1e4, -100.0, -88.0, -20.0, -0.0, 0.0, 20.0, 88.0, 100.0, 1e4])
+    at = torch.randint(0, len(pick), c.pre.shape, generator=torch.Generator().manual_seed(1))
+    c.pre.copy_(pick[at].to(BF16))
+    if glu:                                          # up half and dy of ordinary size: the products stay finite
+        c.pre[:, c.I:] = torch.randn(rows, c.I, device=dev()).to(BF16)
+    else:
+        c.pre.clamp_(max=1e4)
+    dpre = torch.empty_like(c.pre)
+    N.moe_expert_down_backward(c.shape, c.dy, c.offsets, c.w2, c.pre, None, dpre, None, c.ws)
+    c.status()
+    want, bound = c.dpre_ref()
+    # below 2^-126 a sigmoid may flush to zero: its value times |g| + 1, the largest factor here
+    check(dpre, want, bound + 2.0 ** -126 * 4e2 * (want.abs() + 1), "dpre")
+
+
 @pytest.mark.parametrize("bad", [[0, 60, 50, 100], [-1, 30, 60, 100], [0, 30, 60, 101], [0, 1 << 30, 60, 100],
                                  [0, 30, -(1 << 31), 100]], ids=str)
 def test_bad_bucket_bounds_are_reported_and_move_nothing(bad):
