@@ -158,11 +158,15 @@ __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 
 
 // max(z, 0) that keeps a NaN.
 __device__ __forceinline__ float relu(float z) { return z <= 0.f ? 0.f : z; }
-// d silu(g) u: dg = dh u s (1 + g (1 - s)), du = dh g s, s = sigmoid(g).
+// d silu(g) u: dg = dh u s (1 + g (1 - s)), du = dh g s, s = sigmoid(g).  s and 1 - s
+// come from e = exp(-|g|), so neither cancels and a saturated gate keeps its small s
+// (1 / (1 + exp(-g)) drops it from |g| = 87 on).
 __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& dg, float& du) {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-g));
+    const float e = __expf(-fabsf(g));
+    const float r = __fdividef(1.0f, 1.0f + e), er = e * r;
+    const float s = g >= 0.f ? r : er, t = g >= 0.f ? er : r;      // t = 1 - s
     const float gs = g * s;
-    dg = dh * u * fmaf(gs, 1.0f - s, s);
+    dg = dh * u * fmaf(gs, t, s);
     du = dh * gs;
 }
 
