@@ -13,6 +13,10 @@ namespace {
 
 WsHeader* header(void* ws) { return static_cast<WsHeader*>(ws); }
 
+float* partials(const moe_shape& s, void* ws) {
+    return reinterpret_cast<float*>(static_cast<char*>(ws) + ws_layout(s).partials);
+}
+
 bool aligned_or_null(const void* p, uintptr_t a) { return p == nullptr || aligned(p, a); }
 
 bool is_type(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F32; }
@@ -168,7 +172,7 @@ moe_status moe_gate_backward(const moe_shape* shape, const float* dlogits, const
     g.out = dx; g.ldo = s.hidden;
     g.wb = x; g.wM = s.experts; g.wN = s.hidden;
     g.wout = dw_gate; g.wmode = wgrad;
-    return launch_expert_grad(g, header(ws), st);
+    return launch_expert_grad(g, partials(s, ws), header(ws), st);
 }
 
 moe_status moe_expert_up_train(const moe_shape* shape, const uint16_t* x_perm, const int32_t* offsets,
@@ -213,7 +217,7 @@ moe_status moe_expert_down_backward(const moe_shape* shape, const uint16_t* dy_p
     g.pre = pre; g.act = s.act;
     g.wb = h; g.wM = s.hidden; g.wN = s.inter;
     g.wout = dw2; g.wmode = wgrad;
-    return launch_expert_grad(g, header(ws), static_cast<cudaStream_t>(stream));
+    return launch_expert_grad(g, partials(s, ws), header(ws), static_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_expert_up_backward(const moe_shape* shape, const uint16_t* dpre, const int32_t* offsets,
@@ -233,7 +237,7 @@ moe_status moe_expert_up_backward(const moe_shape* shape, const uint16_t* dpre, 
     g.out = dx_perm; g.ldo = s.hidden;
     g.wb = x_perm; g.wM = up_rows(s); g.wN = s.hidden;
     g.wout = dw13; g.wmode = wgrad;
-    return launch_expert_grad(g, header(ws), static_cast<cudaStream_t>(stream));
+    return launch_expert_grad(g, partials(s, ws), header(ws), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

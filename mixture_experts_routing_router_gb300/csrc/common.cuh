@@ -42,8 +42,62 @@ constexpr size_t kAlign = 1024;
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// The gradient GEMMs of one projection (gemm_grad.cu): rows form K x N over `rows`
+// rows in `groups` buckets (N == 0: absent), weights form wM x wN (wM == 0: absent).
+// A form whose tiles each reduce over far more steps than a CTA pair's share of the
+// whole has its reduction split into parts; their FP32 results, kept in the workspace,
+// are summed by a second kernel.  grad_plan says into how many parts (1: not split).
+struct GradDims {
+    long long rows;
+    int groups, K, N, wM, wN;
+};
+struct GradPlan { int r, w; };
+constexpr int kGradTile = 256, kGradStep = 64, kGradPairs = 76;   // output tile, reduction step, CTA pairs
+constexpr int kGradMinSteps = 8;      // of a part: a ring's worth
+inline GradPlan grad_plan(const GradDims& d) {
+    auto tiles = [](long long n) { return (n + kGradTile - 1) / kGradTile; };
+    const long long used = d.rows < d.groups ? d.rows : d.groups;
+    const long long rt = d.N > 0 ? (d.rows / kGradTile + used) * tiles(d.N) : 0;          // at most
+    const long long wt = d.wM > 0 ? (long long)d.groups * tiles(d.wM) * tiles(d.wN) : 0;
+    const long long kr = (d.K + kGradStep - 1) / kGradStep, kw = d.rows / d.groups / kGradStep + 1;   // steps; average bucket
+    // A pair's share in steps (a tile takes five at least, for its output).  The longest
+    // tile decides the time when it is well above the share; 20 steps more is what the
+    // second kernel and the FP32 round trip cost.  Parts of a third of the share even out.
+    auto cost = [](long long k) { return k > 5 ? k : 5; };
+    long long share = (rt * cost(kr) + wt * cost(kw)) / kGradPairs;
+    if (share < kGradMinSteps) share = kGradMinSteps;
+    const long long unit = share / 3 > kGradMinSteps ? share / 3 : kGradMinSteps;
+    auto parts = [&](long long n, long long k) { return n < 1 || k <= share + 20 ? 1LL : (k + unit / 2) / unit; };
+    const long long r = parts(rt, kr), w = parts(wt, kw);
+    return {(int)(r > 16 ? 16 : r), (int)(w > 16 ? 16 : w)};
+}
+// Floats of the rows form's and of both forms' partial results.
+inline size_t grad_rows_partials(const GradDims& d, const GradPlan& n) { return n.r > 1 ? (size_t)n.r * d.rows * d.N : 0; }
+inline size_t grad_partials(const GradDims& d) {
+    const GradPlan n = grad_plan(d);
+    return grad_rows_partials(d, n) + (n.w > 1 ? (size_t)n.w * d.groups * d.wM * d.wN : 0);
+}
+// The most that any gradient call of this shape keeps (both forms, or one of them).
+inline size_t grad_scratch_bytes(const moe_shape& s) {
+    const long long R = (long long)s.tokens * s.top_k;
+    const int up = (s.act == MOE_ACT_SWIGLU ? 2 : 1) * s.inter;
+    const GradDims all[3] = {{R, s.experts, s.hidden, s.inter, s.hidden, s.inter},
+                             {R, s.experts, up, s.hidden, up, s.hidden},
+                             {s.tokens, 1, s.experts, s.hidden, s.experts, s.hidden}};
+    size_t most = 0;
+    for (const GradDims& d : all)
+        for (int form = 1; form < 4; ++form) {
+            GradDims one = d;
+            if (!(form & 1)) one.N = 0;
+            if (!(form & 2)) one.wM = 0;
+            const size_t b = 4 * grad_partials(one);
+            most = b > most ? b : most;
+        }
+    return most;
+}
+
 struct WsLayout {
-    size_t hdr, flags, rank, h_shared;        // stage regions
+    size_t hdr, flags, rank, h_shared, partials;        // stage regions
     size_t stage_end;                         // bytes the stage calls need
     size_t counts, offsets, ids, w, dest, sorted_pair, x_perm, h, y_perm, y_shared;
     size_t sync;                              // moe_layer's fused decode FFN: its counters
@@ -61,6 +115,7 @@ inline WsLayout ws_layout(const moe_shape& s) {
     L.flags = o;        o = align_up(o + (size_t)L.count_tiles * E * 8, kAlign);
     L.rank = o;         o = align_up(o + R * 4, kAlign);
     L.h_shared = o;     o = align_up(o + T * (size_t)s.shared * (size_t)s.shared_inter * 2, kAlign);
+    L.partials = o;     o = align_up(o + grad_scratch_bytes(s), kAlign);
     L.stage_end = o;
     L.counts = o;       o = align_up(o + E * 4, kAlign);
     L.offsets = o;      o = align_up(o + (E + 1) * 4, kAlign);
@@ -613,7 +668,8 @@ struct ExpertGradProblem {
     const uint16_t* wb; int wM, wN;
     void* wout; int wmode;
 };
-moe_status launch_expert_grad(const ExpertGradProblem& p, WsHeader* hdr, cudaStream_t st);
+// partials: the workspace's region of grad_scratch_bytes.
+moe_status launch_expert_grad(const ExpertGradProblem& p, float* partials, WsHeader* hdr, cudaStream_t st);
 // FP32 [rows, cols] to BF16 [rows, cols8], zeros past cols.
 cudaError_t launch_round_rows(long long rows, int cols, int cols8, const float* a, uint16_t* b, cudaStream_t st);
 

@@ -25,6 +25,11 @@
 // layer 8 us less, and the short tiles of the weights form fill the last, partly
 // filled round of the long tiles of the rows form.
 //
+// A form with few output tiles and long reductions (grad_plan) has them split: a pair
+// takes one part of one tile and writes its FP32 partial result to the workspace, and
+// join_kernel adds the parts in order and does what the epilogue would have done.  One
+// expert of 565 rows, H 6432, I 416: 57 us in one piece, 42 split.
+//
 // The weights form reduces over a group's rows.  A last step of fewer than 64
 // rows also loads rows of the next group (or past the last one); each CTA's fixer
 // warp waits for that step's copies on a barrier of its own, zeroes the rows past
@@ -46,7 +51,7 @@ namespace {
 
 enum Act : int { kSwiGLU = 0, kReLU2 = 1, kPlain = 2 };      // what the rows form's epilogue applies
 
-constexpr int TM = 256, TN = 256, BK = 64;        // output tile of the pair, reduction step
+constexpr int TM = kGradTile, TN = kGradTile, BK = kGradStep;   // output tile of the pair, reduction step
 constexpr int HALF = 128;                         // rows / columns each CTA contributes
 constexpr int OP_BYTES = HALF * BK * 2;           // 16 KiB an operand and CTA
 constexpr int BOX_BYTES = 64 * BK * 2;            // one 64 x 64 box of an MN-major operand
@@ -74,6 +79,11 @@ struct GParams {
     // weights form (wM == 0: not asked for)
     int wM, wN, wmode;               // wmode: moe_wgrad
     void* wout;
+    // SPLIT: parts of each form's reduction, and their results [rsplit][a_rows][N] and
+    // [wsplit][groups][wM][wN] (not used where there is one part)
+    int rsplit, wsplit;
+    float* rpart;
+    float* wpart;
 };
 
 struct Ctl {
@@ -222,9 +232,8 @@ __device__ __forceinline__ void bf16_tile(uint32_t tl, bool empty, int rows, int
 
 // FP32 output (stored or added to), 32 columns at a time.
 template <typename F>
-__device__ __forceinline__ void f32_tile(const GParams& p, uint32_t tl, bool empty, int rows, int n0, float* out,
+__device__ __forceinline__ void f32_tile(uint32_t tl, bool empty, int rows, int n0, int N, bool add, float* out,
                                          uint8_t* s, int lane, F&& release) {
-    const bool add = p.wmode == MOE_WGRAD_F32_ADD;
 #pragma unroll 1
     for (int c = 0; c < EPI_COLS / 32; ++c) {
         const int u = lane & 7, col = n0 + c * 32 + u * 4;
@@ -233,7 +242,7 @@ __device__ __forceinline__ void f32_tile(const GParams& p, uint32_t tl, bool emp
         for (int i = 0; i < 8; ++i) {
             const int r = i * 4 + (lane >> 3);
             old[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (add && r < rows && col < p.wN) old[i] = *reinterpret_cast<const float4*>(out + (size_t)r * p.wN + col);
+            if (add && r < rows && col < N) old[i] = *reinterpret_cast<const float4*>(out + (size_t)r * N + col);
         }
         uint32_t v[32];
         if (!empty) {
@@ -251,8 +260,8 @@ __device__ __forceinline__ void f32_tile(const GParams& p, uint32_t tl, bool emp
         for (int i = 0; i < 8; ++i) {
             const int r = i * 4 + (lane >> 3);
             const uint4 w = *unit128(s, r, u);
-            if (r < rows && col < p.wN)
-                *reinterpret_cast<float4*>(out + (size_t)r * p.wN + col) =
+            if (r < rows && col < N)
+                *reinterpret_cast<float4*>(out + (size_t)r * N + col) =
                     make_float4(old[i].x + __uint_as_float(w.x), old[i].y + __uint_as_float(w.y),
                                 old[i].z + __uint_as_float(w.z), old[i].w + __uint_as_float(w.w));
         }
@@ -482,39 +491,60 @@ __device__ __forceinline__ Tile weights_tile(int tile, const int* rstart, const 
 // first `skip` rounds of the (mostly shorter) weights form's tiles, as many as take
 // about as long as that tile: the loop adds up their steps, five at least, which is
 // what writing a tile takes.
+// Split: the same with every part of a tile in its place.
+template <bool SPLIT>
 struct Walk {
-    int nrows, total, pairs, pair, extra, skip, i, s, j;
-    __device__ __forceinline__ Walk(int nrows_, int total_, int pairs_, int pair_, int row_steps, int per_group,
-                                    const int* rcount)
-        : nrows(nrows_), total(total_), pairs(pairs_), pair(pair_), skip(0), i(pair_), s(0) {
+    int nrows, total, pairs, pair, extra, skip, i, s, j;          // counts of parts
+    int rsplit, wsplit, part;                                     // part: of the tile next() returned
+    __device__ __forceinline__ Walk(int row_tiles, int weight_tiles, int pairs_, int pair_, int row_steps, int per_group,
+                                    const int* rcount, int rsplit_, int wsplit_)
+        : pairs(pairs_), pair(pair_), skip(0), i(pair_), s(0), rsplit(rsplit_), wsplit(wsplit_), part(0) {
+        nrows = row_tiles * (SPLIT ? rsplit : 1);
+        total = nrows + weight_tiles * (SPLIT ? wsplit : 1);
+        if (SPLIT) row_steps /= rsplit;
         extra = nrows % pairs;
         if (extra)
             for (int steps = 0; nrows + skip * pairs < total; ++skip) {
-                const int mine = max((rcount[skip * pairs / per_group] + BK - 1) / BK, 5);
+                const int g = skip * pairs / per_group / (SPLIT ? wsplit : 1);
+                const int mine = max((rcount[g] + BK - 1) / BK / (SPLIT ? wsplit : 1), 5);
                 if (steps + mine / 2 >= row_steps) break;
                 steps += mine;
             }
         j = nrows + skip * (pairs - extra) + pair;
     }
-    __device__ __forceinline__ int next() {                       // -1: done
+    // The tile, the rows form's first; -1: done.
+    __device__ __forceinline__ int next() {
         int t;
         if (i < nrows) {
             t = i;
             i += pairs;
-            return t;
-        }
-        if (s < skip && pair >= extra) {
+        } else if (s < skip && pair >= extra) {
             t = nrows + s * (pairs - extra) + pair - extra;
             ++s;
         } else {
             t = j;
             j += pairs;
         }
-        return t < total ? t : -1;
+        if (t >= total) return -1;
+        if (!SPLIT) return t;
+        if (t < nrows) {
+            part = t % rsplit;
+            return t / rsplit;
+        }
+        part = (t - nrows) % wsplit;
+        return nrows / rsplit + (t - nrows) / wsplit;
+    }
+    // The steps of this part of a reduction of nk, and whether it is one of several.
+    __device__ __forceinline__ int parts(bool weights) const { return SPLIT ? (weights ? wsplit : rsplit) : 1; }
+    __device__ __forceinline__ int first(int nk, bool weights) const {
+        return SPLIT ? (int)((long long)nk * part / parts(weights)) : 0;
+    }
+    __device__ __forceinline__ int last(int nk, bool weights) const {
+        return SPLIT ? (int)((long long)nk * (part + 1) / parts(weights)) : nk;
     }
 };
 
-template <int ACT>
+template <int ACT, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
 grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmWA, const __grid_constant__ CUtensorMap tmWB,
@@ -624,7 +654,7 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     volatile int* abort = &ctl->abort;
     const int nk_rows = (p.K + BK - 1) / BK;
     const int nrows = ctl->rows_tiles;
-    Walk walk(nrows, nrows + p.groups * wtm * wtn, npairs, pair, nk_rows, wtm * wtn, rcount);
+    Walk<SPLIT> walk(nrows, p.groups * wtm * wtn, npairs, pair, nk_rows, wtm * wtn, rcount, p.rsplit, p.wsplit);
 
     if (warp == 0) {
         // ---------------- TMA producer (both CTAs) ----------------
@@ -637,7 +667,7 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 const bool weights = tile >= nrows;
                 const Tile t = weights ? weights_tile(tile - nrows, rstart, rcount, wtm, wtn)
                                        : rows_tile(tile, prefix, rstart, rcount, p.groups);
-                const bool swap = !weights && t.partial();
+                const bool swap = !weights && t.partial() && walk.parts(false) == 1;
                 // this CTA's rows (rows form) or columns of A: 128, or half of the padded rows
                 const int a0 = t.m0 + (int)rank * (swap ? t.padded() / 2 : HALF);
                 const int b0 = t.n0 + (int)rank * HALF;
@@ -645,7 +675,7 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 auto load = [&](auto form) {
                     constexpr bool kW = decltype(form)::value;
                     const int nk = kW ? (t.mrows + BK - 1) / BK : nk_rows;
-                    for (int i = 0; i < nk; ++i) {
+                    for (int i = walk.first(nk, kW), end = walk.last(nk, kW); i < end; ++i) {
                         if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), ph ^ 1u, abort)) { ok = false; break; }
                         const uint32_t full_local = smem_u32(&ctl->full[stage]);
                         const uint32_t full_leader = mapa_shared(full_local, 0);
@@ -703,15 +733,16 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 Tile t{};
                 if (weights) t.mrows = rcount[(tile - nrows) / (wtm * wtn)];
                 else t = rows_tile(tile, prefix, rstart, rcount, p.groups);
-                if (t.mrows == 0) continue;
+                const int nk_all = weights ? (t.mrows + BK - 1) / BK : nk_rows;
+                const int i0 = walk.first(nk_all, weights), nk = walk.last(nk_all, weights);
+                if (i0 == nk) continue;
                 if (!mbar_wait_cluster(smem_u32(&ctl->tempty[acc]), aph ^ 1u, abort)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(acc * TN);
                 // A and B: MN-major (boxes of reduction rows) or K-major
                 auto multiply = [&](auto a_mn, auto b_mn, uint32_t idesc) {
                     constexpr bool kAmn = decltype(a_mn)::value, kBmn = decltype(b_mn)::value, kW = kAmn && kBmn;
-                    const int nk = kW ? (t.mrows + BK - 1) / BK : nk_rows;
-                    for (int i = 0; i < nk; ++i) {
+                    for (int i = i0; i < nk; ++i) {
                         if (!mbar_wait_bounded(smem_u32(&ctl->full[stage]), ph, abort)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t sa = smem_base + stage * STAGE_BYTES, sb = sa + OP_BYTES;
@@ -722,13 +753,13 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                             if (!kW || i * BK + kk * 16 < t.mrows)        // slices that hold rows
                                 tc_mma_bf16_pair(d, ad + (uint64_t)kk * (kAmn ? kMnStep : kKStep),
                                                  bd + (uint64_t)kk * (kBmn ? kMnStep : kKStep), idesc,
-                                                 (i > 0 || kk > 0) ? 1u : 0u);
+                                                 (i > i0 || kk > 0) ? 1u : 0u);
                         tc_commit_pair_mc(smem_u32(&ctl->empty[stage]), (uint16_t)3);
                         if (++stage == stages) { stage = 0; ph ^= 1u; }
                     }
                 };
                 if (weights) multiply(std::true_type{}, std::true_type{}, idesc_bf16_f32(TM, TN) | kMajorA | kMajorB);
-                else if (t.partial()) multiply(std::true_type{}, std::false_type{}, idesc_bf16_f32(TM, t.padded()) | kMajorA);
+                else if (t.partial() && walk.parts(false) == 1) multiply(std::true_type{}, std::false_type{}, idesc_bf16_f32(TM, t.padded()) | kMajorA);
                 else multiply(std::false_type{}, std::true_type{}, idesc_bf16_f32(TM, TN) | kMajorB);
                 if (!ok) break;
                 tc_commit_pair_mc(smem_u32(&ctl->tfull[acc]), (uint16_t)3);
@@ -758,9 +789,11 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const int m0 = t.m0 + (int)rank * HALF + q * 32;
             const int rows = (weights ? p.wM : t.mrows) - m0;            // of its 32 rows, those below the bound
             const int n0 = t.n0 + c0;
-            const bool empty = weights && t.mrows == 0;                  // zeros, no accumulator
-            const bool swap = !weights && t.partial();
-            if (ACT != kPlain && !weights) {
+            const int nk = weights ? (t.mrows + BK - 1) / BK : nk_rows;
+            const bool empty = walk.first(nk, weights) == walk.last(nk, weights);   // zeros, no accumulator
+            const bool parts = walk.parts(weights) > 1;
+            const bool swap = !weights && t.partial() && !parts;
+            if (ACT != kPlain && !weights && !parts) {
                 if (!swap)
                     act_prefetch<ACT == kSwiGLU>(p, m0, rows, t.row0, n0, epi, lane);
                 else
@@ -783,12 +816,16 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 __syncwarp();
                 if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&ctl->tempty[acc]), 0));
             };
-            if (swap) {
+            if (SPLIT && parts) {
+                float* out = weights ? p.wpart + (((size_t)walk.part * p.groups + t.g) * p.wM + m0) * p.wN
+                                     : p.rpart + ((size_t)walk.part * p.a_rows + t.row0 + m0) * p.N;
+                f32_tile(tl, empty, rows, n0, weights ? p.wN : p.N, false, out, epi, lane, release);
+            } else if (swap) {
                 swapped_tile<ACT>(p, tl - c0, t.mrows - t.m0, t.row0 + t.m0, t.n0 + (int)rank * HALF + q * 32,
                                   (warp - 2) / 4, epi, lane, release);
             } else if (weights && p.wmode != MOE_WGRAD_BF16) {
                 if (!(empty && p.wmode == MOE_WGRAD_F32_ADD))
-                    f32_tile(p, tl, empty, rows, n0,
+                    f32_tile(tl, empty, rows, n0, p.wN, p.wmode == MOE_WGRAD_F32_ADD,
                              static_cast<float*>(p.wout) + ((size_t)t.g * p.wM + m0) * p.wN, epi, lane, release);
             } else if (ACT != kPlain && !weights) {
                 act_tile<ACT == kSwiGLU>(p, tl, m0, rows, t.row0, n0, epi, lane, release);
@@ -810,12 +847,14 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
         uint32_t pph = 0;                          // parity of part[s] and fixed[s] in bit s
         bool ok = true;
         for (int tile; ok && (tile = walk.next()) >= 0;) {
+            const bool weights = tile >= nrows;
             int nk = nk_rows, rem = 0;
-            if (tile >= nrows) {
+            if (weights) {
                 const int mrows = rcount[(tile - nrows) / (wtm * wtn)];
                 nk = (mrows + BK - 1) / BK;
-                rem = mrows & (BK - 1);
+                if (walk.last(nk, true) == nk && walk.first(nk, true) < nk) rem = mrows & (BK - 1);
             }
+            nk = walk.last(nk, weights) - walk.first(nk, weights);   // this part's
             if (rem) {
                 const int s = (stage + nk - 1) % stages;
                 const uint32_t parity = (pph >> s) & 1u;
@@ -862,13 +901,13 @@ size_t smem_bytes(int groups, int stages) {
     return 1024 + (size_t)stages * STAGE_BYTES + EPI_WARPS * EPI_BYTES + sizeof(Ctl) + 3 * (size_t)(groups + 1) * 4;
 }
 
-template <int ACT>
+template <int ACT, bool SPLIT>
 moe_status launch_grad(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mwa, const CUtensorMap& mwb,
                        const GParams& gp, cudaStream_t st) {
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(grad_gemm_pair_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr_err = cudaFuncSetAttribute(grad_gemm_pair_kernel<ACT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         MAX_DYN_SMEM);
     });
     if (attr_err != cudaSuccess) {
@@ -876,13 +915,99 @@ moe_status launch_grad(const CUtensorMap& ma, const CUtensorMap& mb, const CUten
         return MOE_ERR_CUDA;
     }
     const size_t smem = smem_bytes(gp.groups, gp.stages);
-    const cudaError_t e = launch_kernel(grad_gemm_pair_kernel<ACT>, dim3((unsigned)(device_sm_count() & ~1)),
+    const cudaError_t e = launch_kernel(grad_gemm_pair_kernel<ACT, SPLIT>, dim3((unsigned)(device_sm_count() & ~1)),
                                         dim3(THREADS), smem, st, 2, kUsePdl, ma, mb, mwa, mwb, gp);
     if (e != cudaSuccess) {
         set_error("gradient GEMM launch (smem %zu): %s", smem, cudaGetErrorString(e));
         return MOE_ERR_CUDA;
     }
     return MOE_OK;
+}
+
+// Eight consecutive elements of the parts, added in order.
+__device__ __forceinline__ void add_parts(const float* part, size_t stride, int split, float (&f)[8]) {
+    const float4* q = reinterpret_cast<const float4*>(part);
+    float4 a = q[0], b = q[1];
+    for (int s = 1; s < split; ++s) {
+        q = reinterpret_cast<const float4*>(part + (size_t)s * stride);
+        const float4 c = q[0], d = q[1];
+        a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
+        b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
+    }
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+__device__ __forceinline__ uint4 pack8f(const float (&f)[8]) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+// The split reductions' second half: sums the parts and stores them as the epilogue of
+// an unsplit one does, eight elements a thread (N and wN are multiples of 8).
+__global__ void __launch_bounds__(256)
+join_kernel(const GParams p, int act) {
+    pdl_wait();
+    pdl_trigger();
+    int bad = 0;                                  // as in the GEMM: nothing moves then
+    for (int g = threadIdx.x; p.offsets && g < p.groups; g += blockDim.x)
+        bad |= p.offsets[g] < 0 || p.offsets[g + 1] < p.offsets[g] || p.offsets[g + 1] > p.a_rows;
+    if (__syncthreads_or(bad)) return;
+    const int lo = p.offsets ? p.offsets[0] : 0, hi = p.offsets ? p.offsets[p.groups] : p.a_rows;
+    const int nv = p.N / 8;
+    const long long nr = p.rsplit > 1 ? (long long)(hi - lo) * nv : 0;
+    const long long nw = p.wsplit > 1 ? (long long)p.groups * p.wM * (p.wN / 8) : 0;
+    const size_t rstride = (size_t)p.a_rows * p.N, wstride = (size_t)p.groups * p.wM * p.wN;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < nr + nw; i += (long long)gridDim.x * blockDim.x) {
+        float f[8];
+        if (i < nr) {
+            const long long r = lo + i / nv;
+            const int c = (int)(i % nv) * 8;
+            add_parts(p.rpart + r * p.N + c, rstride, p.rsplit, f);
+            __nv_bfloat16* o = p.out + r * p.ldo + c;
+            if (act == kPlain) {
+                *reinterpret_cast<uint4*>(o) = pack8f(f);
+                continue;
+            }
+            const uint4 g4 = *reinterpret_cast<const uint4*>(p.pre + r * p.ldo + c);
+            const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
+            if (act == kReLU2) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[2 * j] *= 2.0f * relu(bf_lo(gw[j]));
+                    f[2 * j + 1] *= 2.0f * relu(bf_hi(gw[j]));
+                }
+                *reinterpret_cast<uint4*>(o) = pack8f(f);
+                continue;
+            }
+            const uint4 u4 = *reinterpret_cast<const uint4*>(p.pre + r * p.ldo + p.up_off + c);
+            const uint32_t uw[4] = {u4.x, u4.y, u4.z, u4.w};
+            float du[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float d0 = f[2 * j], d1 = f[2 * j + 1];
+                swiglu_grad(d0, bf_lo(gw[j]), bf_lo(uw[j]), f[2 * j], du[2 * j]);
+                swiglu_grad(d1, bf_hi(gw[j]), bf_hi(uw[j]), f[2 * j + 1], du[2 * j + 1]);
+            }
+            *reinterpret_cast<uint4*>(o) = pack8f(f);
+            *reinterpret_cast<uint4*>(o + p.up_off) = pack8f(du);
+        } else {
+            const size_t e = (size_t)(i - nr) * 8;
+            add_parts(p.wpart + e, wstride, p.wsplit, f);
+            if (p.wmode == MOE_WGRAD_BF16) {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.wout) + e) = pack8f(f);
+                continue;
+            }
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.wout) + e);
+            float4 a = make_float4(f[0], f[1], f[2], f[3]), b = make_float4(f[4], f[5], f[6], f[7]);
+            if (p.wmode == MOE_WGRAD_F32_ADD) {
+                const int g = (int)(e / ((size_t)p.wM * p.wN));
+                if (p.offsets && p.offsets[g] == p.offsets[g + 1]) continue;    // no rows: left as it is
+                const float4 x = o[0], y = o[1];
+                a = make_float4(x.x + a.x, x.y + a.y, x.z + a.z, x.w + a.w);
+                b = make_float4(y.x + b.x, y.y + b.y, y.z + b.z, y.w + b.w);
+            }
+            o[0] = a;
+            o[1] = b;
+        }
+    }
 }
 
 // FP32 [rows, cols] to BF16 [rows, cols8], the columns past cols zero.
@@ -933,7 +1058,7 @@ act_kernel(long long rows, int IV, long long ldv, const int32_t* __restrict__ of
 
 }  // namespace
 
-moe_status launch_expert_grad(const ExpertGradProblem& g, WsHeader* hdr, cudaStream_t st) {
+moe_status launch_expert_grad(const ExpertGradProblem& g, float* partials, WsHeader* hdr, cudaStream_t st) {
     const long long rows_tiles = g.out ? (g.rows / TM + g.groups) * (((long long)g.N + TN - 1) / TN) : 0;
     const long long w_tiles = g.wout ? (long long)g.groups * ((g.wM + TM - 1) / TM) * ((g.wN + TN - 1) / TN) : 0;
     if (device_sm_count() < 2 || rows_tiles + w_tiles > INT_MAX / 2 ||
@@ -968,9 +1093,28 @@ moe_status launch_expert_grad(const ExpertGradProblem& g, WsHeader* hdr, cudaStr
     gp.a_rows = (int)g.rows;
     gp.stages = smem_bytes(g.groups, MAX_STAGES) <= (size_t)MAX_DYN_SMEM ? MAX_STAGES : MAX_STAGES - 1;
     gp.hdr = hdr;
-    if (!g.out || !g.pre) return launch_grad<kPlain>(ma, mb, mwa, mwb, gp, st);
-    return g.act == MOE_ACT_SWIGLU ? launch_grad<kSwiGLU>(ma, mb, mwa, mwb, gp, st)
-                                   : launch_grad<kReLU2>(ma, mb, mwa, mwb, gp, st);
+    const GradDims dims = {g.rows, g.groups, gp.K, gp.N, gp.wM, gp.wN};
+    const GradPlan n = grad_plan(dims);
+    gp.rsplit = n.r;
+    gp.wsplit = n.w;
+    gp.rpart = partials;
+    gp.wpart = partials + grad_rows_partials(dims, n);
+    const int act = !g.out || !g.pre ? kPlain : g.act == MOE_ACT_SWIGLU ? kSwiGLU : kReLU2;
+    if (n.r == 1 && n.w == 1) {
+        if (act == kPlain) return launch_grad<kPlain, false>(ma, mb, mwa, mwb, gp, st);
+        return act == kSwiGLU ? launch_grad<kSwiGLU, false>(ma, mb, mwa, mwb, gp, st)
+                              : launch_grad<kReLU2, false>(ma, mb, mwa, mwb, gp, st);
+    }
+    // an activation is only applied here when the rows form itself is not split
+    const int here = n.r > 1 ? (int)kPlain : act;
+    const moe_status r = here == kPlain    ? launch_grad<kPlain, true>(ma, mb, mwa, mwb, gp, st)
+                         : here == kSwiGLU ? launch_grad<kSwiGLU, true>(ma, mb, mwa, mwb, gp, st)
+                                           : launch_grad<kReLU2, true>(ma, mb, mwa, mwb, gp, st);
+    if (r != MOE_OK) return r;
+    const long long vecs = ((n.r > 1 ? g.rows * gp.N : 0) + (n.w > 1 ? (long long)g.groups * gp.wM * gp.wN : 0)) / 8;
+    long long blocks = (vecs + 255) / 256;
+    if (blocks > device_sm_count() * 8LL) blocks = device_sm_count() * 8LL;
+    return from_cuda(launch_kernel(join_kernel, dim3((unsigned)blocks), dim3(256), 0, st, 1, kUsePdl, gp, act));
 }
 
 cudaError_t launch_round_rows(long long rows, int cols, int cols8, const float* a, uint16_t* b, cudaStream_t st) {

@@ -90,6 +90,10 @@ SHAPES = [(8, 8), (64, 64), (136, 72), (256, 512), (320, 264), (1024, 264)]
 @pytest.mark.parametrize("glu", [True, False], ids=["swiglu", "relu2"])
 def test_backward_matches_the_formulas(counts, hi, glu):
     c = Case(COUNTS[counts], *hi, glu, seed=len(counts) + hi[0], spare=3 if counts == "steps" else 0)
+    run_and_check(c, COUNTS[counts])
+
+
+def run_and_check(c, counts):
     dpre = Guarded((c.R, c.up), BF16)
     dw2, dw13 = Guarded((c.E, c.H, c.I), BF16), Guarded((c.E, c.up, c.H), BF16)
     dx = Guarded((c.R, c.H), BF16)
@@ -97,7 +101,7 @@ def test_backward_matches_the_formulas(counts, hi, glu):
     N.moe_expert_up_backward(c.shape, c.dpre_in, c.offsets, c.x, c.w13, dx.t, dw13.t, c.ws)
     c.status()
     assert all(b.intact() for b in (dpre, dw2, dw13, dx))
-    v, n = c.valid, max(COUNTS[counts])
+    v, n = c.valid, max(counts)
     check(dpre.t[:v], *c.dpre_ref(), "dpre")
     want, mag = ref.weights_grad(c.dy, c.h, c.offsets)
     check(dw2.t, want, ref.sum_bound(n, mag) + ref.U_BF16 * want.abs(), "dw2")
@@ -109,6 +113,41 @@ def test_backward_matches_the_formulas(counts, hi, glu):
     canary = torch.full((2,), 0xA5, dtype=torch.uint8, device=dev()).view(BF16)
     if c.R > v:
         assert torch.equal(dx.t[v:].contiguous().view(torch.int16), canary.view(torch.int16).expand(c.R - v, c.H))
+
+
+# few output tiles and long reductions: split over the CTA pairs, in every residue of the
+# last 64-row step and with parts of no step at all
+SPLIT = [([300], 4096, 64), ([2000], 64, 40), ([5], 6432, 416), ([1031, 1], 72, 1480), ([1400, 0, 2600], 136, 200),
+         ([0, 1600], 8, 8), ([64 * 20], 256, 256), ([3, 2500], 520, 24)]
+
+
+@pytest.mark.parametrize("case", SPLIT, ids=str)
+@pytest.mark.parametrize("glu", [True, False], ids=["swiglu", "relu2"])
+def test_split_reductions_match_the_formulas(case, glu):
+    counts, H, I = case
+    c = Case(counts, H, I, glu, seed=H + I, spare=0 if len(counts) == 1 else 2 * len(counts) - sum(counts) % len(counts))
+    run_and_check(c, counts)
+    # float32, stored and added, without the rows form
+    want, mag = ref.weights_grad(c.dy, c.h, c.offsets)
+    bound = ref.sum_bound(max(counts), mag) + 2 * ref.U_F32 * want.abs()
+    dw = Guarded(tuple(want.shape), F32)
+    N.moe_expert_down_backward(c.shape, c.dy, c.offsets, None, None, c.h, None, dw.t, c.ws)
+    c.status()
+    check(dw.t, want, bound, "dw2")
+    old = torch.randn(want.shape, device=dev())
+    dw.t.copy_(old)
+    N.moe_expert_down_backward(c.shape, c.dy, c.offsets, None, None, c.h, None, dw.t, c.ws, add=True)
+    c.status()
+    check(dw.t, want + old.to(D), bound + 2 * ref.U_F32 * old.to(D).abs(), "dw2 +=")
+    empty = [e for e, m in enumerate(counts) if m == 0]
+    assert torch.equal(dw.t[empty], old[empty]) and dw.intact()
+    # the rows form alone, and again: the same bits
+    a, b = torch.zeros_like(c.pre), torch.zeros_like(c.pre)
+    for t in (a, b):
+        N.moe_expert_down_backward(c.shape, c.dy, c.offsets, c.w2, c.pre, None, t, None, c.ws)
+    c.status()
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    check(a[:c.valid], *c.dpre_ref(), "dpre alone")
 
 
 @pytest.mark.parametrize("counts", ["ones", "steps", "ring"])
@@ -220,7 +259,8 @@ def test_up_train_keeps_its_pre_activations(counts, glu):
 
 
 @pytest.mark.parametrize("size", [(1, 8, 1), (5, 72, 3), (64, 256, 16), (300, 136, 33), (257, 1000, 240),
-                                  (130, 64, 1024), (2000, 520, 100)], ids=str)
+                                  (130, 64, 1024), (2000, 520, 100), (6000, 264, 40),
+                                  (5000, 1032, 8)], ids=str)
 def test_gate_backward(size):
     T, H, E = size
     g = torch.Generator().manual_seed(T)
