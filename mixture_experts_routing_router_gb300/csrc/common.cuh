@@ -63,6 +63,8 @@ inline GradPlan grad_plan(const GradDims& d) {
     // A pair's share in steps (a tile takes five at least, for its output).  The longest
     // tile decides the time when it is well above the share; 20 steps more is what the
     // second kernel and the FP32 round trip cost.  Parts of a third of the share even out.
+    // Over 94 shapes of 1 to 34 experts against no split: 0.90 to 1.92 times as fast,
+    // geometric mean 1.03.  Splitting from 24 steps on lost 7 to 12 % with 19 to 34 tiles.
     auto cost = [](long long k) { return k > 5 ? k : 5; };
     long long share = (rt * cost(kr) + wt * cost(kw)) / kGradPairs;
     if (share < kGradMinSteps) share = kGradMinSteps;

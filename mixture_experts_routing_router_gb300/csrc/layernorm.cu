@@ -22,9 +22,9 @@
 // [blocks][2][H] FP32 array, summed by a second small kernel in a fixed order.
 // Rows wider than 16384 columns (8192 FP32 columns backward) run the looping
 // kernels, which re-read the row through L2.
-// Measured, [16384, 7168] BF16: forward 77 us, 6.1 TB/s (weights from L1: 159 us;
+// Measured, [16384, 7168] BF16: forward 76 us, 6.2 TB/s (weights from L1: 159 us;
 // 16 columns a thread, the issue slots going to the reductions: 99 us); backward
-// with the residual's gradient 157 us, 6.0 TB/s (three passes over x and dy: 507).
+// with the residual's gradient 154 us, 6.1 TB/s (three passes over x and dy: 507).
 #include "common.cuh"
 
 #include <mutex>
