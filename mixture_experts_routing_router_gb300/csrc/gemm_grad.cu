@@ -147,7 +147,8 @@ __device__ __forceinline__ void fence_release_smem_cluster() {
     asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
 }
 // All threads of both CTAs have got here; no memory is handed over (a releasing barrier
-// waits for the last tile's stores: 0.9 us of a 64-token layer's 21).
+// waits for the last tile's stores: 0.9 us of a 64-token layer's 21).  It does not wait
+// for arrivals on the other CTA's barriers either: each has been waited for before.
 __device__ __forceinline__ void cluster_sync_relaxed() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -712,6 +713,11 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 if (weights) load(std::true_type{});
                 else load(std::false_type{});
             }
+            // every arrival that the MMAs' commits still send to this CTA is in before it exits
+            for (int s = 0; ok && s < stages; ++s) {
+                if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), ph ^ 1u, abort)) ok = false;
+                if (++stage == stages) { stage = 0; ph ^= 1u; }
+            }
             if (!ok) {
                 // as in the forward pair kernel: the leader waits for the phases it
                 // armed, the peer (which cannot wait on a remote barrier) adds a delay
@@ -763,6 +769,13 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 else multiply(std::false_type{}, std::true_type{}, idesc_bf16_f32(TM, TN) | kMajorB);
                 if (!ok) break;
                 tc_commit_pair_mc(smem_u32(&ctl->tfull[acc]), (uint16_t)3);
+                acc ^= 1;
+                if (acc == 0) aph ^= 1u;
+            }
+            // and every one that the peer's epilogue sends to the leader: the closing barrier
+            // does not wait for them, and after this CTA they would hit the next one's memory
+            for (int a = 0; ok && a < 2; ++a) {
+                if (!mbar_wait_cluster(smem_u32(&ctl->tempty[acc]), aph ^ 1u, abort)) ok = false;
                 acc ^= 1;
                 if (acc == 0) aph ^= 1u;
             }

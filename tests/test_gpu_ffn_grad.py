@@ -150,6 +150,24 @@ def test_split_reductions_match_the_formulas(case, glu):
     check(a[:c.valid], *c.dpre_ref(), "dpre alone")
 
 
+def test_calls_back_to_back_keep_their_bits():
+    """The pair's last arrivals are in before a kernel ends: the next one, of another
+    layout on the same SMs, gets the results it gets alone."""
+    c = Case([77, 0, 300, 64, 9], 264, 136, True, seed=3)
+    pre, h = torch.empty_like(c.pre), torch.empty_like(c.h)
+    runs = []
+    for _ in range(100):
+        dpre, dx = torch.zeros_like(c.pre), torch.zeros_like(c.x)
+        dw2, dw13 = torch.zeros_like(c.w2), torch.zeros_like(c.w13)
+        N.moe_expert_down_backward(c.shape, c.dy, c.offsets, c.w2, c.pre, c.h, dpre, dw2, c.ws)
+        N.moe_expert_up_train(c.shape, c.x, c.offsets, c.w13, pre, h, c.ws)
+        N.moe_expert_up_backward(c.shape, dpre, c.offsets, c.x, c.w13, dx, dw13, c.ws)
+        runs.append((dpre, dx, dw2, dw13, pre.clone(), h.clone()))
+    for got in runs[1:]:
+        assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(runs[0], got))
+    c.status()
+
+
 @pytest.mark.parametrize("counts", ["ones", "steps", "ring"])
 def test_float32_weight_gradients_and_accumulation(counts):
     c = Case(COUNTS[counts], 136, 72, True, seed=5)
