@@ -146,12 +146,6 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
 __device__ __forceinline__ void fence_release_smem_cluster() {
     asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
 }
-// All threads of both CTAs have got here; no memory is handed over (a releasing barrier
-// waits for the last tile's stores: 0.9 us of a 64-token layer's 21).  It does not wait
-// for arrivals on the other CTA's barriers either: each has been waited for before.
-__device__ __forceinline__ void cluster_sync_relaxed() {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, uint32_t bar_cluster, int x, int y,
                                                  int z) {
     asm volatile(
@@ -772,8 +766,8 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 acc ^= 1;
                 if (acc == 0) aph ^= 1u;
             }
-            // and every one that the peer's epilogue sends to the leader: the closing barrier
-            // does not wait for them, and after this CTA they would hit the next one's memory
+            // and every one that the peer's epilogue sends to the leader: after this CTA
+            // they would hit the next one's memory
             for (int a = 0; ok && a < 2; ++a) {
                 if (!mbar_wait_cluster(smem_u32(&ctl->tempty[acc]), aph ^ 1u, abort)) ok = false;
                 acc ^= 1;
@@ -902,7 +896,7 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
 
     tc_fence_before();
     __syncthreads();
-    cluster_sync_relaxed();      // the leader's MMAs have drained before either CTA frees its TMEM
+    cluster_sync();              // the leader's MMAs have drained before either CTA frees its TMEM
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
