@@ -235,6 +235,20 @@ __device__ __forceinline__ bool wait_armed_stages(uint32_t full0, int stages, lo
     return all;
 }
 
+// A TMA producer's last step in a kernel of CTA pairs, in both CTAs: wait for the
+// arrivals that the leader's multicast commits still send to this CTA's ring of
+// `empty` barriers (8 bytes apart from `empty0`; `stage` and `ph` are the next stage
+// to fill and its phase; stages never used pass at once).  Neither the accumulator's
+// barrier nor the closing cluster barrier covers them, and after this CTA they would
+// hit the shared memory of the next one on the SM.
+__device__ __forceinline__ bool drain_ring(uint32_t empty0, int stages, int stage, uint32_t ph, volatile int* abort) {
+    for (int s = 0; s < stages; ++s) {
+        if (!mbar_wait_bounded(empty0 + 8u * (uint32_t)stage, ph ^ 1u, abort)) return false;
+        if (++stage == stages) { stage = 0; ph ^= 1u; }
+    }
+    return true;
+}
+
 // Last resort after wait_armed_stages failed: a fixed 1 ms delay.
 __device__ __forceinline__ void settle_delay() {
     const unsigned long long t0 = globaltimer_ns();

@@ -643,6 +643,7 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_c
                     if (++stage == P_STAGES) { stage = 0; ph ^= 1u; }
                 }
             }
+            if (ok) ok = drain_ring(smem_u32(&ctl->empty[0]), P_STAGES, stage, ph, abort);
             if (!ok) {
                 // Both CTAs' copies of a stage complete on the leader's full barrier,
                 // armed for the pair's bytes: the leader waits for the phases it armed

@@ -707,11 +707,7 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 if (weights) load(std::true_type{});
                 else load(std::false_type{});
             }
-            // every arrival that the MMAs' commits still send to this CTA is in before it exits
-            for (int s = 0; ok && s < stages; ++s) {
-                if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), ph ^ 1u, abort)) ok = false;
-                if (++stage == stages) { stage = 0; ph ^= 1u; }
-            }
+            if (ok) ok = drain_ring(smem_u32(&ctl->empty[0]), stages, stage, ph, abort);
             if (!ok) {
                 // as in the forward pair kernel: the leader waits for the phases it
                 // armed, the peer (which cannot wait on a remote barrier) adds a delay

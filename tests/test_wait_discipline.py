@@ -1,0 +1,52 @@
+"""Rules on the kernels' waits that no GPU test can show without hanging a GPU when
+they are broken, checked on the sources (CPU).
+
+A role is a brace block of a kernel; the checks look at what encloses a wait and
+at which barriers a kernel's commits reach.
+"""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "mixture_experts_routing_router_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        text = f.read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def kernels(name):
+    """(name, body) of every __global__ function of a file."""
+    text, out = source(name), []
+    for m in re.finditer(r"__global__[^{;]*?(\w+)\s*\((?:[^(){};]|\([^(){};]*\))*\)\s*\{", text):
+        depth, i = 1, m.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(text[i], 0)
+            i += 1
+        out.append((m.group(1), text[m.end():i - 1]))
+    return out
+
+
+def test_the_parser_finds_the_kernels():
+    assert {n for n, _ in kernels("gemm.cu")} >= {"grouped_gemm_kernel", "grouped_gemm_pair_kernel"}
+    assert "grad_gemm_pair_kernel" in {n for n, _ in kernels("gemm_grad.cu")}
+
+
+@pytest.mark.parametrize("name", ["gemm.cu", "gemm_grad.cu"])
+def test_multicast_commits_are_awaited_before_a_cta_exits(name):
+    """A commit to a stage barrier of both CTAs of a pair arrives in the peer without
+    the peer's having to wait for it; each producer drains its ring before it leaves,
+    or the arrival may land in the shared memory of the next CTA on that SM."""
+    seen = 0
+    for kernel, body in kernels(name):
+        if not re.search(r"tc_commit_pair_mc\(smem_u32\(&ctl->empty\[", body):
+            continue
+        seen += 1
+        producer = body[body.index("if (warp == 0) {"):body.index("} else if (warp == 1) {")]
+        assert "drain_ring(smem_u32(&ctl->empty[0])" in producer, kernel
+        assert "rank" not in re.search(r"if \(([^\n]*)\) ok = drain_ring", producer).group(1), kernel   # both CTAs
+    assert seen == 1
