@@ -219,6 +219,13 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
+// A whole warp's wait.  Lanes can give up apart (one sees the abort flag, another the
+// phase); the verdict is the warp's, so that none leaves for the closing barrier while
+// the rest go on to a warp-wide instruction and wait for it there without a limit.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort)) != 0;
+}
+
 // After a TMA producer gave up: wait (bounded, on a never-set abort flag of its
 // own) for the full-barrier phases of the last stages it armed, so that no bulk
 // copy it issued is still writing this CTA's shared memory when the CTA exits.

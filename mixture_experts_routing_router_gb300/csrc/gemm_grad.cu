@@ -135,6 +135,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
         }
     }
 }
+__device__ __forceinline__ bool mbar_wait_cluster_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort)) != 0;
+}
 // Relaxed arrival on a barrier of the pair: it hands back an accumulator, whose
 // reads tcgen05.fence::before_thread_sync orders; a release would also wait for the
 // warp's stores of the tile before.
@@ -804,7 +807,7 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                                                      (warp - 2) / 4, lane);
             }
             if (!empty) {
-                if (!mbar_wait_bounded(smem_u32(&ctl->tfull[acc]), aph, abort)) {
+                if (!mbar_wait_warp(smem_u32(&ctl->tfull[acc]), aph, abort)) {
                     if (lane == 0) {
                         raise_status(p.hdr, MOE_ERR_TIMEOUT);
                         p.hdr->timeout_site = kSiteGradEpilogue;
@@ -862,7 +865,7 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 const int s = (stage + nk - 1) % stages;
                 const uint32_t parity = (pph >> s) & 1u;
                 pph ^= 1u << s;
-                if (!mbar_wait_bounded(smem_u32(&ctl->part[s]), parity, abort)) { ok = false; break; }
+                if (!mbar_wait_warp(smem_u32(&ctl->part[s]), parity, abort)) { ok = false; break; }
                 const int end = (rem + 15) & ~15;
                 // four boxes of 128-byte rows; the swizzle stays inside a row
                 for (int i = lane; i < 4 * (end - rem) * 8; i += 32) {
@@ -878,7 +881,7 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                         mbar_arrive_relaxed(mapa_shared(smem_u32(&ctl->fixed[s]), 0));
                     }
                 } else {
-                    if (!mbar_wait_cluster(smem_u32(&ctl->fixed[s]), parity, abort)) { ok = false; break; }
+                    if (!mbar_wait_cluster_warp(smem_u32(&ctl->fixed[s]), parity, abort)) { ok = false; break; }
                     if (lane == 0) mbar_arrive(smem_u32(&ctl->full[s]));
                 }
             }

@@ -50,3 +50,34 @@ def test_multicast_commits_are_awaited_before_a_cta_exits(name):
         assert "drain_ring(smem_u32(&ctl->empty[0])" in producer, kernel
         assert "rank" not in re.search(r"if \(([^\n]*)\) ok = drain_ring", producer).group(1), kernel   # both CTAs
     assert seen == 1
+
+
+def enclosing(body, pos):
+    """The texts before the open braces that enclose `pos`, outermost first."""
+    heads, last = [], 0
+    for i, c in enumerate(body[:pos]):
+        if c == "{":
+            heads.append(body[last:i])
+        elif c == "}":
+            heads.pop()
+        if c in "{};":
+            last = i + 1
+    return heads
+
+
+SINGLE = re.compile(r"\b(?:lane|tid) == 0\b")
+KERNELS_THAT_WAIT = ["gemm_grad.cu"]
+
+
+@pytest.mark.parametrize("name", KERNELS_THAT_WAIT)
+def test_a_warp_gives_up_a_wait_as_a_whole(name):
+    """Lanes that decide apart whether a wait ran out part for good: some reach the
+    closing barrier, the rest a warp-wide instruction, and both wait for ever.  A wait
+    outside a block of one thread has to be the warp's."""
+    waits = 0
+    for kernel, body in kernels(name):
+        for m in re.finditer(r"\b(mbar_wait_bounded|mbar_wait_cluster|drain_ring|wait_armed_stages)\(", body):
+            waits += 1
+            assert any(SINGLE.search(h) for h in enclosing(body, m.start())), \
+                f"{kernel}: {body[m.start():m.start() + 70]!r}"
+    assert waits > 4
