@@ -432,7 +432,7 @@ decode_ffn_kernel(const __grid_constant__ CUtensorMap tmX,     // x_perm: 16-row
             const int N = dn ? p.H : p.I;
             uint16_t* obase = dn ? p.y_perm : p.h;
             const int n = nt * FBM + 32 * q + lane;             // weight row = output column
-            if (!mbar_wait_bounded(smem_u32(&ctl->tfull[acc]), aph, abort)) {
+            if (!mbar_wait_warp(smem_u32(&ctl->tfull[acc]), aph, abort)) {
                 if (lane == 0) {
                     raise_status(p.hdr, MOE_ERR_TIMEOUT);
                     p.hdr->timeout_site = kSiteDecodeFfn;

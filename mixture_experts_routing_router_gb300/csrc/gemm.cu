@@ -436,7 +436,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         uint32_t aph = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
             const Tile t = decode_tile<MODE == kGemmSwiGLU || MODE == kGemmReLU2>(tile, prefix, rstart, rcount, p, ntn, C::BMT);
-            if (!mbar_wait_bounded(smem_u32(&ctl->tfull[acc]), aph, abort)) {
+            if (!mbar_wait_warp(smem_u32(&ctl->tfull[acc]), aph, abort)) {
                 if (lane == 0) {
                     raise_status(p.hdr, MOE_ERR_TIMEOUT);
                     p.hdr->timeout_site = kSiteGemmEpilogue;
@@ -703,7 +703,7 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_c
         uint32_t aph = 0;
         for (int tile = pair; tile < total; tile += npairs) {
             const Tile t = decode_tile<MODE == kGemmSwiGLU || MODE == kGemmReLU2>(tile, prefix, rstart, rcount, p, ntn, P_BMT);
-            if (!mbar_wait_bounded(smem_u32(&ctl->tfull[acc]), aph, abort)) {
+            if (!mbar_wait_warp(smem_u32(&ctl->tfull[acc]), aph, abort)) {
                 if (lane == 0) {
                     raise_status(p.hdr, MOE_ERR_TIMEOUT);
                     p.hdr->timeout_site = kSiteGemmEpilogue;
@@ -1080,8 +1080,8 @@ grouped_gemm_q_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
         bool ok = true;
         for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
             for (int i = 0; i < nk; ++i) {
-                if (!mbar_wait_bounded(smem_u32(&ctl->full[stage]), ph, abort) ||
-                    !mbar_wait_bounded(smem_u32(&ctl->cempty[cs]), cph ^ 1u, abort)) { ok = false; break; }
+                if (!mbar_wait_warp(smem_u32(&ctl->full[stage]), ph, abort) ||
+                    !mbar_wait_warp(smem_u32(&ctl->cempty[cs]), cph ^ 1u, abort)) { ok = false; break; }
                 const uint8_t* codes = smem + stage * QG::STAGE_BYTES + A_BYTES;
                 // NVFP4: this quarter's block scale of each pass, from the stage (0x100
                 // marks a block past K: zeros; rows past the weights arrive as scale 0)
@@ -1162,7 +1162,7 @@ grouped_gemm_q_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 scl[j] = col < p.N ? __ldg(qp.wscale + row) * undo : 0.f;
             }
             __syncwarp();
-            if (!mbar_wait_bounded(smem_u32(&ctl->tfull[acc]), aph, abort)) {
+            if (!mbar_wait_warp(smem_u32(&ctl->tfull[acc]), aph, abort)) {
                 if (lane == 0) {
                     raise_status(p.hdr, MOE_ERR_TIMEOUT);
                     p.hdr->timeout_site = kSiteGemmEpilogue;

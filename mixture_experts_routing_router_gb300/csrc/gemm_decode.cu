@@ -504,7 +504,7 @@ decode_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             const int rows = gcnt[it / ntn];
             for (int c0 = 0; c0 < rows && ok; c0 += nb) {
                 for (int i = 0; i < nk && ok; ++i) {
-                    if (!mbar_wait_bounded(smem_u32(&ctl->full[stage]), ph, abort)) { ok = false; break; }
+                    if (!mbar_wait_warp(smem_u32(&ctl->full[stage]), ph, abort)) { ok = false; break; }
                     const uint8_t* st = smem + (size_t)stage * p.stage_bytes;
                     const uint8_t* src = st + w_off + (size_t)r * DBK8;
                     uint4 scl[NW];                              // NVFP4: the row's 16 block scales, per box
@@ -513,7 +513,7 @@ decode_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                         for (int wb = 0; wb < NW; ++wb)
                             scl[wb] = *reinterpret_cast<const uint4*>(st + p.s_off + wb * S4_BYTES + r * 16);
                     for (int ch = 0; ch < NCH; ++ch) {
-                        if (!mbar_wait_bounded(smem_u32(&ctl->cempty[cs]), cph ^ 1u, abort)) { ok = false; break; }
+                        if (!mbar_wait_warp(smem_u32(&ctl->cempty[cs]), cph ^ 1u, abort)) { ok = false; break; }
                         tc_fence_after();                       // after the MMAs that read slot cs
                         const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + p.a_col +
                                                (uint32_t)(cs * SLOT_COLS) + (uint32_t)(hf * (CK / 4));
@@ -592,7 +592,7 @@ decode_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                 if (MODE == kGemmSwiGLU) su = p.wscale[(size_t)g * p.b_group_rows + p.up_off + n] * kUndo;
             }
             for (int c0 = 0; c0 < rows; c0 += nb) {
-                if (!mbar_wait_bounded(smem_u32(&ctl->tfull[acc]), aph, abort)) {
+                if (!mbar_wait_warp(smem_u32(&ctl->tfull[acc]), aph, abort)) {
                     if (lane == 0) {
                         raise_status(p.hdr, MOE_ERR_TIMEOUT);
                         p.hdr->timeout_site = kSiteGemmDecode;

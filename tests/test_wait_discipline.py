@@ -66,7 +66,7 @@ def enclosing(body, pos):
 
 
 SINGLE = re.compile(r"\b(?:lane|tid) == 0\b")
-KERNELS_THAT_WAIT = ["gemm_grad.cu"]
+KERNELS_THAT_WAIT = ["gemm.cu", "gemm_decode.cu", "decode_ffn.cu", "gemm_grad.cu"]
 
 
 @pytest.mark.parametrize("name", KERNELS_THAT_WAIT)
