@@ -701,17 +701,29 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_c
         const int q = warp & 3;
         int acc = 0;
         uint32_t aph = 0;
+        bool live = true;
         for (int tile = pair; tile < total; tile += npairs) {
             const Tile t = decode_tile<MODE == kGemmSwiGLU || MODE == kGemmReLU2>(tile, prefix, rstart, rcount, p, ntn, P_BMT);
-            if (!mbar_wait_warp(smem_u32(&ctl->tfull[acc]), aph, abort)) {
+            const int rows_t = t.mrows - t.mt * P_BMT;
+            if (live && !mbar_wait_warp(smem_u32(&ctl->tfull[acc]), aph, abort)) {
                 if (lane == 0) {
                     raise_status(p.hdr, MOE_ERR_TIMEOUT);
                     p.hdr->timeout_site = kSiteGemmEpilogue;
                 }
-                break;
+                live = false;
+            }
+            if (!live) {
+                // the other warps may still be in a swapped SwiGLU tile, whose named
+                // barriers count on this one: it meets them, tile by tile
+                if (MODE == kGemmSwiGLU && rows_t < P_BMT) {
+                    for (int c = 0; c < ((rows_t + 15) & ~15); c += 16) {
+                        epi_bar_sync();
+                        epi_bar_sync();
+                    }
+                }
+                continue;
             }
             tc_fence_after();
-            const int rows_t = t.mrows - t.mt * P_BMT;
             if (rows_t < P_BMT) {
                 // Swapped: TMEM lane = this CTA's weight row i (its B half), column j =
                 // row j of the tile.  SwiGLU: lanes 0..63 gate, 64..127 up of output

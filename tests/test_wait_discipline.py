@@ -81,3 +81,20 @@ def test_a_warp_gives_up_a_wait_as_a_whole(name):
             assert any(SINGLE.search(h) for h in enclosing(body, m.start())), \
                 f"{kernel}: {body[m.start():m.start() + 70]!r}"
     assert waits > 4
+
+
+def test_a_warp_that_gave_up_still_meets_named_barriers():
+    """The epilogue warps of the CTA-pair kernel meet at named barriers in a swapped
+    SwiGLU tile.  A warp that gave up its wait and left would strand the others there:
+    it stays in the tile loop and meets as many of them."""
+    met = 0
+    for kernel, body in kernels("gemm.cu"):
+        at = [m.start() for m in re.finditer(r"epi_bar_sync\(\);", body)]
+        if not at:
+            continue
+        met += 1
+        dead = [i for i in at if any(h.strip() == "if (!live)" for h in enclosing(body, i))]
+        assert len(dead) == len(at) - len(dead) == 2, kernel
+        give_up = body.index("kSiteGemmEpilogue")
+        assert body[give_up:].split("}")[1].split() == ["live", "=", "false;"], kernel
+    assert met == 1
