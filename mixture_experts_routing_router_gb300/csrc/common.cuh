@@ -226,18 +226,25 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort)) != 0;
 }
 
-// After a TMA producer gave up: wait (bounded, on a never-set abort flag of its
-// own) for the full-barrier phases of the last stages it armed, so that no bulk
-// copy it issued is still writing this CTA's shared memory when the CTA exits.
+// Wait until the phase has completed or the clock has passed `end`.
+__device__ __forceinline__ bool mbar_wait_until(uint32_t bar, uint32_t parity, unsigned long long end) {
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() > end) return false;
+    return true;
+}
+
+// After a TMA producer gave up: wait (on no abort flag, and kWaitLimitNs for all of
+// them together) for the full-barrier phases of the last stages it armed, so that no
+// bulk copy it issued is still writing this CTA's shared memory when the CTA exits.
 // `armed` counts the stages armed since the kernel began; the ring has `stages`
 // slots whose full barriers are 8 bytes apart from `full0`.  Returns false if
 // some phase did not complete within the limit.
 __device__ __forceinline__ bool wait_armed_stages(uint32_t full0, int stages, long long armed) {
-    volatile int never = 0;
+    const unsigned long long end = globaltimer_ns() + kWaitLimitNs;
     bool all = true;
     for (long long j = armed > stages ? armed - stages : 0; j < armed; ++j) {
         const uint32_t bar = full0 + 8u * (uint32_t)(j % stages);
-        if (!mbar_wait_bounded(bar, (uint32_t)((j / stages) & 1), &never)) all = false;
+        if (!mbar_wait_until(bar, (uint32_t)((j / stages) & 1), end)) all = false;
     }
     return all;
 }

@@ -144,6 +144,25 @@ __device__ __forceinline__ bool mbar_wait_cluster_warp(uint32_t bar, uint32_t pa
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
+// wait_armed_stages for one CTA of a pair (`rank`).  The copies of a whole step count
+// on the leader's full barrier, which only the leader can wait on; those of a partial
+// step (stage s last armed so: bit s of `on_part`) on a barrier of each CTA's own,
+// whose uses `part_uses` counts modulo two -- the leader's full barrier then waits for
+// the fixer, which may have given up as well.
+__device__ __forceinline__ bool wait_armed_pair_stages(uint32_t full0, uint32_t part0, int stages, long long armed,
+                                                       uint32_t on_part, uint32_t part_uses, uint32_t rank) {
+    const unsigned long long end = globaltimer_ns() + kWaitLimitNs;
+    bool all = true;
+    for (long long j = armed > stages ? armed - stages : 0; j < armed; ++j) {
+        const uint32_t s = (uint32_t)(j % stages);
+        if ((on_part >> s) & 1u) {
+            if (!mbar_wait_until(part0 + 8u * s, ((part_uses >> s) & 1u) ^ 1u, end)) all = false;
+        } else if (rank != 0 || !mbar_wait_until(full0 + 8u * s, (uint32_t)((j / stages) & 1), end)) {
+            all = false;
+        }
+    }
+    return all;
+}
 // Release, at cluster scope, of this CTA's shared memory only.  (A full release
 // waits for every store of the thread: it took the fixer 0.5 us and more a tile.)
 __device__ __forceinline__ void fence_release_smem_cluster() {
@@ -661,6 +680,7 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             uint32_t ph = 0;
             bool ok = true;
             long long armed = 0;
+            uint32_t on_part = 0, part_uses = 0;     // for wait_armed_pair_stages
             for (int tile; ok && (tile = walk.next()) >= 0;) {
                 const bool weights = tile >= nrows;
                 const Tile t = weights ? weights_tile(tile - nrows, rstart, rcount, wtm, wtn)
@@ -678,11 +698,14 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                         const uint32_t full_local = smem_u32(&ctl->full[stage]);
                         const uint32_t full_leader = mapa_shared(full_local, 0);
                         const uint32_t sa = smem_base + stage * STAGE_BYTES, sb = sa + OP_BYTES;
+                        on_part &= ~(1u << stage);
                         if (kW) {
                             const int y = t.row0 + i * BK;
                             if (t.mrows - i * BK < BK) {
                                 // partial step: counted on this CTA's own barrier, for its fixer
                                 const uint32_t part = smem_u32(&ctl->part[stage]);
+                                on_part |= 1u << stage;
+                                part_uses ^= 1u << stage;
                                 mbar_arrive_expect_tx(part, STAGE_BYTES);
                                 tma_load_2d(sa, &tmWA, part, a0, y);
                                 tma_load_2d(sa + BOX_BYTES, &tmWA, part, a0 + 64, y);
@@ -712,9 +735,11 @@ grad_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             }
             if (ok) ok = drain_ring(smem_u32(&ctl->empty[0]), stages, stage, ph, abort);
             if (!ok) {
-                // as in the forward pair kernel: the leader waits for the phases it
-                // armed, the peer (which cannot wait on a remote barrier) adds a delay
-                if (rank != 0 || !wait_armed_stages(smem_u32(&ctl->full[0]), stages, armed)) settle_delay();
+                // the copies issued land before the CTA exits; the closing cluster barrier
+                // holds the peer until the leader has seen its whole steps' too
+                if (!wait_armed_pair_stages(smem_u32(&ctl->full[0]), smem_u32(&ctl->part[0]), stages, armed, on_part,
+                                            part_uses, rank))
+                    settle_delay();
                 raise_status(p.hdr, MOE_ERR_TIMEOUT);
                 p.hdr->timeout_site = kSiteGradProducer;
             }
