@@ -977,13 +977,15 @@ __global__ void __launch_bounds__(256)
 join_kernel(const GParams p, int act) {
     pdl_wait();
     pdl_trigger();
-    int bad = 0;                                  // as in the GEMM: nothing moves then
+    // refused bounds, as in the GEMM: no bucket has rows, so no row is written and each
+    // expert's weight gradient is that of an empty bucket (the GEMM left zeros as its parts)
+    int bad = 0;
     for (int g = threadIdx.x; p.offsets && g < p.groups; g += blockDim.x)
         bad |= p.offsets[g] < 0 || p.offsets[g + 1] < p.offsets[g] || p.offsets[g + 1] > p.a_rows;
-    if (__syncthreads_or(bad)) return;
+    const bool none = __syncthreads_or(bad) != 0;
     const int lo = p.offsets ? p.offsets[0] : 0, hi = p.offsets ? p.offsets[p.groups] : p.a_rows;
     const int nv = p.N / 8;
-    const long long nr = p.rsplit > 1 ? (long long)(hi - lo) * nv : 0;
+    const long long nr = p.rsplit > 1 && !none ? (long long)(hi - lo) * nv : 0;
     const long long nw = p.wsplit > 1 ? (long long)p.groups * p.wM * (p.wN / 8) : 0;
     const size_t rstride = (size_t)p.a_rows * p.N, wstride = (size_t)p.groups * p.wM * p.wN;
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < nr + nw; i += (long long)gridDim.x * blockDim.x) {
@@ -1030,7 +1032,7 @@ join_kernel(const GParams p, int act) {
             float4 a = make_float4(f[0], f[1], f[2], f[3]), b = make_float4(f[4], f[5], f[6], f[7]);
             if (p.wmode == MOE_WGRAD_F32_ADD) {
                 const int g = (int)(e / ((size_t)p.wM * p.wN));
-                if (p.offsets && p.offsets[g] == p.offsets[g + 1]) continue;    // no rows: left as it is
+                if (none || (p.offsets && p.offsets[g] == p.offsets[g + 1])) continue;    // no rows: left as it is
                 const float4 x = o[0], y = o[1];
                 a = make_float4(x.x + a.x, x.y + a.y, x.z + a.z, x.w + a.w);
                 b = make_float4(y.x + b.x, y.y + b.y, y.z + b.z, y.w + b.w);

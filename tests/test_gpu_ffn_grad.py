@@ -362,3 +362,36 @@ def test_gradients_against_differences():
         # independent errors of the gradient's own size): four of them, five sigma
         tol = 5 * 2 * 0.5 * ref.U_BF16 * grad.to(D).norm()
         assert abs(got - diff) <= tol, (i, float(got), float(diff), float(tol))
+
+
+# in one piece, with the weights form split, with both forms split
+@pytest.mark.parametrize("case", [([30, 30, 40], 72, 40), ([1950, 1950], 64, 40), ([2600], 2400, 64)], ids=str)
+@pytest.mark.parametrize("bad", ["decreasing", "negative", "past the end"])
+def test_refused_bounds_leave_the_weight_gradient_of_empty_buckets(case, bad):
+    counts, H, I = case
+    c = Case(counts, H, I, True, seed=11)
+    b = c.offsets.tolist()
+    if bad == "decreasing":
+        b[0], b[1] = b[1], b[0]
+    elif bad == "negative":
+        b[0] = -1
+    else:
+        b[-1] = c.R + 1
+    offsets = torch.tensor(b, dtype=torch.int32, device=dev())
+
+    def calls(dw2, dw13, add=False):
+        N.moe_expert_down_backward(c.shape, c.dy, offsets, c.w2, c.pre, c.h, torch.empty_like(c.pre), dw2, c.ws, add=add)
+        assert N.moe_status_read(c.ws) == N.MOE_ERR_INVALID_ROUTE
+        N.moe_expert_up_backward(c.shape, c.dpre_in, offsets, c.x, c.w13, torch.empty_like(c.x), dw13, c.ws, add=add)
+        assert N.moe_status_read(c.ws) == N.MOE_ERR_INVALID_ROUTE
+        N.moe_expert_up_backward(c.shape, c.dpre_in, offsets, c.x, None, None, dw13, c.ws, add=add)   # its own plan
+        assert N.moe_status_read(c.ws) == N.MOE_ERR_INVALID_ROUTE
+
+    for dtype in (BF16, F32):
+        dw2, dw13 = Guarded((c.E, c.H, c.I), dtype), Guarded((c.E, c.up, c.H), dtype)
+        calls(dw2.t, dw13.t)
+        assert torch.all(dw2.t == 0) and torch.all(dw13.t == 0) and dw2.intact() and dw13.intact()
+    old2, old13 = torch.randn(c.E, c.H, c.I, device=dev()), torch.randn(c.E, c.up, c.H, device=dev())
+    dw2, dw13 = old2.clone(), old13.clone()
+    calls(dw2, dw13, add=True)
+    assert torch.equal(dw2, old2) and torch.equal(dw13, old13)
