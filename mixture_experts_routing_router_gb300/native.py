@@ -166,7 +166,7 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         # the current device's current stream, without building a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -195,7 +195,7 @@ def workspace(shape: moe_shape, device="cuda") -> torch.Tensor:
 
 
 def _wsb(ws):
-    return ws.numel() * ws.element_size()
+    return ws.nbytes
 
 
 def moe_route(shape, logits, topk_ids, topk_w, ws, stream=None):
@@ -375,28 +375,63 @@ def moe_layernorm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, scratch,
                                         _stream(stream)), "moe_layernorm_backward")
 
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _arg(t, dtype, n, what):
+    """The address of a tensor with `n` elements of `dtype` at least (a kernel reads or
+    writes that many); None and plain addresses pass as they are."""
+    try:
+        if t.dtype is dtype and t.numel() >= n and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        return _ptr(t)
+    if t.dtype is not dtype or t.numel() < n:
+        raise ValueError(f"{what}: {dtype} with {n} elements at least expected, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _up(shape):
+    return 2 * shape.inter if shape.act == MOE_ACT_SWIGLU else shape.inter
+
+
 def moe_combine_backward(shape, dout, y_perm, dest, topk_w, dy_perm, dtopk_w, ws, stream=None):
     """Gradient of moe_combine: dy_perm, and dtopk_w unless it is None."""
-    _check(lib().moe_combine_backward(ctypes.byref(shape), _ptr(dout), _ptr(y_perm), _ptr(dest), _ptr(topk_w),
-                                      _ptr(dy_perm), _ptr(dtopk_w), _ptr(ws), _wsb(ws), _stream(stream)),
+    T, H = shape.tokens, shape.hidden
+    R = T * shape.top_k
+    _check(lib().moe_combine_backward(ctypes.byref(shape), _arg(dout, _BF16, T * H, "dout"),
+                                      _arg(y_perm, _BF16, R * H, "y_perm"), _arg(dest, _I32, R, "dest"),
+                                      _arg(topk_w, _F32, R, "topk_w"), _arg(dy_perm, _BF16, R * H, "dy_perm"),
+                                      _arg(dtopk_w, _F32, R, "dtopk_w"), _ptr(ws), _wsb(ws), _stream(stream)),
            "moe_combine_backward")
 
 
 def moe_dispatch_backward(shape, dx_perm, dest, dx, ws, stream=None, add=None):
     """Gradient of moe_dispatch's row copy, plus `add`."""
-    _check(lib().moe_dispatch_backward(ctypes.byref(shape), _ptr(dx_perm), _ptr(dest), _ptr(add), _ptr(dx), _ptr(ws),
-                                       _wsb(ws), _stream(stream)), "moe_dispatch_backward")
+    T, H = shape.tokens, shape.hidden
+    R = T * shape.top_k
+    _check(lib().moe_dispatch_backward(ctypes.byref(shape), _arg(dx_perm, _BF16, R * H, "dx_perm"),
+                                       _arg(dest, _I32, R, "dest"), _arg(add, _BF16, T * H, "add"),
+                                       _arg(dx, _BF16, T * H, "dx"), _ptr(ws), _wsb(ws), _stream(stream)),
+           "moe_dispatch_backward")
 
 
 def moe_route_backward(shape, topk_ids, topk_w, dtopk_w, dlogits, ws, stream=None):
-    _check(lib().moe_route_backward(ctypes.byref(shape), _ptr(topk_ids), _ptr(topk_w), _ptr(dtopk_w), _ptr(dlogits),
-                                    _ptr(ws), _wsb(ws), _stream(stream)), "moe_route_backward")
+    T = shape.tokens
+    R = T * shape.top_k
+    _check(lib().moe_route_backward(ctypes.byref(shape), _arg(topk_ids, _I32, R, "topk_ids"),
+                                    _arg(topk_w, _F32, R, "topk_w"), _arg(dtopk_w, _F32, R, "dtopk_w"),
+                                    _arg(dlogits, _F32, T * shape.experts, "dlogits"), _ptr(ws), _wsb(ws),
+                                    _stream(stream)), "moe_route_backward")
 
 
 def moe_route_sigmoid_backward(shape, logits, topk_ids, route_scale, dtopk_w, dlogits, ws, stream=None):
-    _check(lib().moe_route_sigmoid_backward(ctypes.byref(shape), _ptr(logits), _ptr(topk_ids), float(route_scale),
-                                            _ptr(dtopk_w), _ptr(dlogits), _ptr(ws), _wsb(ws), _stream(stream)),
-           "moe_route_sigmoid_backward")
+    T, E = shape.tokens, shape.experts
+    R = T * shape.top_k
+    _check(lib().moe_route_sigmoid_backward(ctypes.byref(shape), _arg(logits, _F32, T * E, "logits"),
+                                            _arg(topk_ids, _I32, R, "topk_ids"), float(route_scale),
+                                            _arg(dtopk_w, _F32, R, "dtopk_w"), _arg(dlogits, _F32, T * E, "dlogits"),
+                                            _ptr(ws), _wsb(ws), _stream(stream)), "moe_route_sigmoid_backward")
 
 
 def _wgrad(dw, add):
@@ -410,31 +445,49 @@ def _wgrad(dw, add):
     return MOE_WGRAD_BF16
 
 
+def _dw(dw, n, what):
+    """The address of a weight gradient of `n` elements, of either type `_wgrad` takes."""
+    return None if dw is None else _arg(dw, _F32 if dw.dtype is _F32 else _BF16, n, what)
+
+
 def moe_gate_backward(shape, dlogits, x, w_gate, dlogits_bf16, dx, dw_gate, ws, stream=None, add=False):
     """dx (None: skipped) and dw_gate (None: skipped; bfloat16 or float32, `add` accumulates into
     float32) from dlogits, rounded into dlogits_bf16 [T, 8 * ceil(E / 8)] on the way."""
-    _check(lib().moe_gate_backward(ctypes.byref(shape), _ptr(dlogits), _ptr(x), _ptr(w_gate), _ptr(dlogits_bf16),
-                                   _ptr(dx), _ptr(dw_gate), _wgrad(dw_gate, add), _ptr(ws), _wsb(ws),
-                                   _stream(stream)), "moe_gate_backward")
+    T, H, E = shape.tokens, shape.hidden, shape.experts
+    _check(lib().moe_gate_backward(ctypes.byref(shape), _arg(dlogits, _F32, T * E, "dlogits"),
+                                   _arg(x, _BF16, T * H, "x"), _arg(w_gate, _BF16, E * H, "w_gate"),
+                                   _arg(dlogits_bf16, _BF16, T * ((E + 7) // 8 * 8), "dlogits_bf16"),
+                                   _arg(dx, _BF16, T * H, "dx"), _dw(dw_gate, E * H, "dw_gate"),
+                                   _wgrad(dw_gate, add), _ptr(ws), _wsb(ws), _stream(stream)), "moe_gate_backward")
 
 
 def moe_expert_up_train(shape, x_perm, offsets, w13, pre, h, ws, stream=None):
     """Up projection that also keeps its pre-activations for the backward pass."""
-    _check(lib().moe_expert_up_train(ctypes.byref(shape), _ptr(x_perm), _ptr(offsets), _ptr(w13), _ptr(pre), _ptr(h),
+    R, H, E, I, up = shape.tokens * shape.top_k, shape.hidden, shape.experts, shape.inter, _up(shape)
+    _check(lib().moe_expert_up_train(ctypes.byref(shape), _arg(x_perm, _BF16, R * H, "x_perm"),
+                                     _arg(offsets, _I32, E + 1, "offsets"), _arg(w13, _BF16, E * up * H, "w13"),
+                                     _arg(pre, _BF16, R * up, "pre"), _arg(h, _BF16, R * I, "h"),
                                      _ptr(ws), _wsb(ws), _stream(stream)), "moe_expert_up_train")
 
 
 def moe_expert_down_backward(shape, dy_perm, offsets, w2, pre, h, dpre, dw2, ws, stream=None, add=False):
     """dpre (None: skipped) and dw2 (None: skipped; bfloat16 or float32, `add` accumulates into float32)."""
-    _check(lib().moe_expert_down_backward(ctypes.byref(shape), _ptr(dy_perm), _ptr(offsets), _ptr(w2), _ptr(pre),
-                                          _ptr(h), _ptr(dpre), _ptr(dw2), _wgrad(dw2, add), _ptr(ws), _wsb(ws),
-                                          _stream(stream)), "moe_expert_down_backward")
+    R, H, E, I, up = shape.tokens * shape.top_k, shape.hidden, shape.experts, shape.inter, _up(shape)
+    _check(lib().moe_expert_down_backward(ctypes.byref(shape), _arg(dy_perm, _BF16, R * H, "dy_perm"),
+                                          _arg(offsets, _I32, E + 1, "offsets"), _arg(w2, _BF16, E * H * I, "w2"),
+                                          _arg(pre, _BF16, R * up, "pre"), _arg(h, _BF16, R * I, "h"),
+                                          _arg(dpre, _BF16, R * up, "dpre"), _dw(dw2, E * H * I, "dw2"),
+                                          _wgrad(dw2, add), _ptr(ws), _wsb(ws), _stream(stream)),
+           "moe_expert_down_backward")
 
 
 def moe_expert_up_backward(shape, dpre, offsets, x_perm, w13, dx_perm, dw13, ws, stream=None, add=False):
     """dx_perm (None: skipped) and dw13 (None: skipped; types as dw2)."""
-    _check(lib().moe_expert_up_backward(ctypes.byref(shape), _ptr(dpre), _ptr(offsets), _ptr(x_perm), _ptr(w13),
-                                        _ptr(dx_perm), _ptr(dw13), _wgrad(dw13, add), _ptr(ws), _wsb(ws),
+    R, H, E, up = shape.tokens * shape.top_k, shape.hidden, shape.experts, _up(shape)
+    _check(lib().moe_expert_up_backward(ctypes.byref(shape), _arg(dpre, _BF16, R * up, "dpre"),
+                                        _arg(offsets, _I32, E + 1, "offsets"), _arg(x_perm, _BF16, R * H, "x_perm"),
+                                        _arg(w13, _BF16, E * up * H, "w13"), _arg(dx_perm, _BF16, R * H, "dx_perm"),
+                                        _dw(dw13, E * up * H, "dw13"), _wgrad(dw13, add), _ptr(ws), _wsb(ws),
                                         _stream(stream)), "moe_expert_up_backward")
 
 
