@@ -76,9 +76,10 @@ class MoEBlock(torch.nn.Module):
 
     Parameters: gamma, beta [hidden] FP32; w_gate [experts, hidden], w13 [experts, up,
     hidden] (up = 2 * inter for SwiGLU, inter for ReLU^2), w2 [experts, hidden, inter]
-    BF16.  The block keeps one workspace for the last token count it saw, so its calls
-    belong on one stream at a time.  Device-side errors (non-finite logits, a bounded
-    wait that ran out) stay in the workspace until ``check`` reads them."""
+    BF16 (of another type, say after ``float()``, the block refuses to run).  The block
+    keeps one workspace for the last token count it saw, so its calls belong on one
+    stream at a time.  Device-side errors (non-finite logits, a bounded wait that ran
+    out) stay in the workspace until ``check`` reads them."""
 
     def __init__(self, hidden, experts, top_k, inter, act=N.MOE_ACT_SWIGLU, eps=1e-5, device="cuda", generator=None):
         super().__init__()
@@ -103,6 +104,13 @@ class MoEBlock(torch.nn.Module):
     def forward(self, x):
         if x.dim() != 2 or x.shape[1] != self.hidden or x.dtype != torch.bfloat16:
             raise ValueError(f"MoEBlock: expected a bfloat16 [tokens, {self.hidden}] input, got {x.dtype} {tuple(x.shape)}")
+        up = 2 * self.inter if self.act == N.MOE_ACT_SWIGLU else self.inter
+        for name, want in (("w_gate", (self.experts, self.hidden)), ("w13", (self.experts, up, self.hidden)),
+                           ("w2", (self.experts, self.hidden, self.inter))):
+            w = getattr(self, name)
+            if w.dtype != torch.bfloat16 or w.shape != want:        # the kernels read them as they lie
+                raise ValueError(f"MoEBlock: {name} must be bfloat16 {want}, got {w.dtype} {tuple(w.shape)} "
+                                 "(gamma and beta may be float32 or bfloat16)")
         shape, ws = self._layer(x.shape[0], x.device)
         return _MoEBlockFn.apply(x.contiguous(), self.gamma, self.beta, self.w_gate, self.w13, self.w2, shape, ws, self.eps)
 
