@@ -21,6 +21,26 @@ import torch
 from . import native as N
 
 
+class _SecondDerivative(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return grads
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("MoEBlock: its gradients cannot be differentiated again")
+
+
+def _differentiable_once(grads):
+    """The gradients, in a graph whose only step raises: without one a loss on them (a
+    gradient penalty) beside another term would lose its gradient without a word.
+    (autograd's once_differentiable raises only where the incoming gradient has a graph.)"""
+    some = [g for g in grads if g is not None]
+    if some:
+        some = iter(_SecondDerivative.apply(some[0].new_zeros((), requires_grad=True), *some))
+    return tuple(None if g is None else next(some) for g in grads)
+
+
 class _MoEBlockFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gamma, beta, w_gate, w13, w2, shape, ws, eps):
@@ -47,6 +67,14 @@ class _MoEBlockFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
+        with torch.no_grad():
+            grads = _MoEBlockFn._gradients(ctx, dout)
+        if torch.is_grad_enabled():           # create_graph
+            grads = _differentiable_once(grads)
+        return (*grads, None, None, None)
+
+    @staticmethod
+    def _gradients(ctx, dout):
         x, gamma, w_gate, w13, w2, n, mean, rstd, ids, w, offsets, dest, x_perm, pre, h, y_perm = ctx.saved_tensors
         shape, ws = ctx.shape, ctx.ws
         want = ctx.needs_input_grad
@@ -68,7 +96,7 @@ class _MoEBlockFn(torch.autograd.Function):
         scratch = N.layernorm_scratch(x.shape[0], x.shape[1], x.device)
         N.moe_layernorm_backward(dn, x, gamma, mean, rstd, dx, dgamma, dbeta, scratch, dres=dout)
         return (dx if want[0] else None, dgamma.to(gamma.dtype) if want[1] else None,
-                dbeta.to(gamma.dtype) if want[2] else None, dw_gate, dw13, dw2, None, None, None)
+                dbeta.to(gamma.dtype) if want[2] else None, dw_gate, dw13, dw2)
 
 
 class MoEBlock(torch.nn.Module):
@@ -79,7 +107,8 @@ class MoEBlock(torch.nn.Module):
     BF16 (of another type, say after ``float()``, the block refuses to run).  The block
     keeps one workspace for the last token count it saw, so its calls belong on one
     stream at a time.  Device-side errors (non-finite logits, a bounded wait that ran
-    out) stay in the workspace until ``check`` reads them."""
+    out) stay in the workspace until ``check`` reads them.  Differentiable once: a second
+    derivative through the block raises."""
 
     def __init__(self, hidden, experts, top_k, inter, act=N.MOE_ACT_SWIGLU, eps=1e-5, device="cuda", generator=None):
         super().__init__()

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from mixture_experts_routing_router_gb300 import block as block_module
 from mixture_experts_routing_router_gb300 import native as N
 from mixture_experts_routing_router_gb300.block import MoEBlock
 
@@ -25,3 +26,48 @@ def test_weights_of_another_type_or_shape_are_refused(act, name):
         setattr(b, name, torch.nn.Parameter(bad(w).contiguous()))
         with pytest.raises(ValueError, match=f"{name} must be bfloat16"):
             b(x)
+
+
+class FakeLibrary:
+    """The native module with calls that compute nothing, for the block's own logic."""
+
+    def __getattr__(self, name):
+        if name.startswith("moe_"):
+            return lambda *a, **k: None
+        return getattr(N, name)
+
+    def workspace(self, shape, device):
+        return torch.zeros(8192, dtype=torch.uint8)
+
+    def layernorm_scratch(self, rows, hidden, device):
+        return torch.zeros(1)
+
+
+def test_second_derivatives_raise(monkeypatch):
+    """A gradient penalty would otherwise lose its gradient without a word."""
+    monkeypatch.setattr(block_module, "N", FakeLibrary())
+    b = block()
+    b.w2.requires_grad_(False)
+    x = torch.zeros(3, 24, dtype=BF16, requires_grad=True)
+    params = [b.gamma, b.beta, b.w_gate, b.w13]
+    for wrt in ([x], [b.gamma], [b.w_gate], [x, *params]):
+        for dout_has_a_graph in (False, True):
+            out = b(x).float()
+            loss = out.square().sum() if dout_has_a_graph else out.sum()
+            grads = torch.autograd.grad(loss, wrt, create_graph=True)
+            assert all(g.shape == t.shape and g.dtype == t.dtype for g, t in zip(grads, wrt))
+            with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+                (loss + sum(g.float().square().sum() for g in grads)).backward()
+
+
+def test_a_graph_that_nothing_asks_for_does_not_matter(monkeypatch):
+    monkeypatch.setattr(block_module, "N", FakeLibrary())
+    b = block()
+    x = torch.zeros(3, 24, dtype=BF16, requires_grad=True)
+    scale = torch.ones((), requires_grad=True)
+    loss = b(x).float().sum() * scale
+    loss.backward(create_graph=True, inputs=[x, scale, *b.parameters()])
+    assert all(p.grad is not None and p.grad.dtype == p.dtype for p in b.parameters())
+    b.zero_grad()
+    b(x.detach()).float().sum().backward()
+    assert all(not p.grad.requires_grad for p in b.parameters())
