@@ -103,7 +103,10 @@ typedef struct moe_shape {
 MOE_API moe_status moe_workspace_size(const moe_shape* shape, size_t* bytes);
 
 /* Zero the workspace's status word and counters.  Call once after allocating
- * a workspace (or allocate it zero-filled).  Enqueued on `stream`. */
+ * a workspace (or allocate it zero-filled).  Enqueued on `stream`.
+ * They are in its first 4096 bytes, all that stays in it between calls: a
+ * workspace serves any shape that it is large enough for, and those bytes
+ * copied to the start of a larger one hand over a status not yet read. */
 MOE_API moe_status moe_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
 /* Routing (ONNX Runtime PR #33963, "Measured CUDA kernel latency": internal

@@ -43,7 +43,8 @@ def _differentiable_once(grads):
 
 class _MoEBlockFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, gamma, beta, w_gate, w13, w2, shape, ws, eps):
+    def forward(ctx, x, gamma, beta, w_gate, w13, w2, block):
+        shape, ws = block._layer(x.shape[0], x.device)
         dev, bf16 = x.device, torch.bfloat16
         T, H, E, k, I = shape.tokens, shape.hidden, shape.experts, shape.top_k, shape.inter
         R, up = T * k, w13.shape[1]
@@ -51,7 +52,7 @@ class _MoEBlockFn(torch.autograd.Function):
         f32 = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)
         b16 = lambda *s: torch.empty(s, dtype=bf16, device=dev)
         n, mean, rstd = torch.empty_like(x), f32(T), f32(T)
-        N.moe_layernorm(x, gamma, beta, eps, n, mean, rstd)
+        N.moe_layernorm(x, gamma, beta, block.eps, n, mean, rstd)
         logits, ids, w = f32(T, E), i32(T, k), f32(T, k)
         N.moe_gate(shape, n, w_gate, logits, ws)
         N.moe_route(shape, logits, ids, w, ws)
@@ -62,7 +63,7 @@ class _MoEBlockFn(torch.autograd.Function):
         N.moe_expert_down(shape, h, offsets, w2, None, y_perm, None, ws)
         N.moe_combine(shape, y_perm, dest, w, None, out, ws, residual=x)
         ctx.save_for_backward(x, gamma, w_gate, w13, w2, n, mean, rstd, ids, w, offsets, dest, x_perm, pre, h, y_perm)
-        ctx.shape, ctx.ws = shape, ws
+        ctx.block = block
         return out
 
     @staticmethod
@@ -71,12 +72,12 @@ class _MoEBlockFn(torch.autograd.Function):
             grads = _MoEBlockFn._gradients(ctx, dout)
         if torch.is_grad_enabled():           # create_graph
             grads = _differentiable_once(grads)
-        return (*grads, None, None, None)
+        return (*grads, None)
 
     @staticmethod
     def _gradients(ctx, dout):
         x, gamma, w_gate, w13, w2, n, mean, rstd, ids, w, offsets, dest, x_perm, pre, h, y_perm = ctx.saved_tensors
-        shape, ws = ctx.shape, ctx.ws
+        shape, ws = ctx.block._layer(x.shape[0], x.device)     # the block's, where check() looks
         want = ctx.needs_input_grad
         like = lambda t, on: torch.empty_like(t) if on else None
         dout = dout.contiguous()
@@ -105,9 +106,10 @@ class MoEBlock(torch.nn.Module):
     Parameters: gamma, beta [hidden] FP32; w_gate [experts, hidden], w13 [experts, up,
     hidden] (up = 2 * inter for SwiGLU, inter for ReLU^2), w2 [experts, hidden, inter]
     BF16 (of another type, say after ``float()``, the block refuses to run).  The block
-    keeps one workspace for the last token count it saw, so its calls belong on one
-    stream at a time.  Device-side errors (non-finite logits, a bounded wait that ran
-    out) stay in the workspace until ``check`` reads them.  Differentiable once: a second
+    keeps one workspace, as large as the largest batch it saw needs, so its calls belong
+    on one stream at a time.  Device-side errors (non-finite logits, a bounded wait that
+    ran out), of any batch and either direction, stay there until ``check`` reads them.
+    Differentiable once: a second
     derivative through the block raises."""
 
     def __init__(self, hidden, experts, top_k, inter, act=N.MOE_ACT_SWIGLU, eps=1e-5, device="cuda", generator=None):
@@ -123,11 +125,22 @@ class MoEBlock(torch.nn.Module):
         self.beta = torch.nn.Parameter(torch.zeros(hidden, device=device))
         self.w_gate, self.w13, self.w2 = draw(experts, hidden), draw(experts, up, hidden), draw(experts, hidden, inter)
         self._shape = self._ws = None
+        self._bytes = 0                       # of workspace that _shape needs
 
     def _layer(self, tokens, device):
-        if self._shape is None or self._shape.tokens != tokens or self._ws.device != device:
-            self._shape = N.make_shape(tokens, self.hidden, self.experts, self.top_k, self.inter, self.act)
-            self._ws = N.workspace(self._shape, device)
+        """The shape of a batch and the block's workspace, grown where the shape needs more.
+        The larger one takes over the header, so a status not yet read stays to be read."""
+        if self._shape is None or self._shape.tokens != tokens:
+            shape = N.make_shape(tokens, self.hidden, self.experts, self.top_k, self.inter, self.act)
+            self._bytes = N.moe_workspace_size(shape)
+            self._shape = shape
+        old = self._ws
+        if old is None or old.device != device or old.nbytes < self._bytes:
+            self._ws = torch.empty(self._bytes, dtype=torch.uint8, device=device)
+            if old is None:
+                N.moe_workspace_init(self._ws)
+            else:
+                self._ws[:N.WORKSPACE_HEADER].copy_(old[:N.WORKSPACE_HEADER])
         return self._shape, self._ws
 
     def forward(self, x):
@@ -140,8 +153,7 @@ class MoEBlock(torch.nn.Module):
             if w.dtype != torch.bfloat16 or w.shape != want:        # the kernels read them as they lie
                 raise ValueError(f"MoEBlock: {name} must be bfloat16 {want}, got {w.dtype} {tuple(w.shape)} "
                                  "(gamma and beta may be float32 or bfloat16)")
-        shape, ws = self._layer(x.shape[0], x.device)
-        return _MoEBlockFn.apply(x.contiguous(), self.gamma, self.beta, self.w_gate, self.w13, self.w2, shape, ws, self.eps)
+        return _MoEBlockFn.apply(x.contiguous(), self.gamma, self.beta, self.w_gate, self.w13, self.w2, self)
 
     def check(self):
         """Synchronise and raise if a kernel of this block's calls reported an error."""

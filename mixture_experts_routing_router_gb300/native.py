@@ -184,9 +184,11 @@ def moe_workspace_size(shape: moe_shape) -> int:
     return n.value
 
 
+WORKSPACE_HEADER = 4096       # bytes at a workspace's start that stay between calls
+
+
 def moe_workspace_init(ws: torch.Tensor, stream=None):
-    _check(lib().moe_workspace_init(_ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-           "moe_workspace_init")
+    _check(lib().moe_workspace_init(_ptr(ws), _wsb(ws), _stream(stream)), "moe_workspace_init")
 
 
 def workspace(shape: moe_shape, device="cuda") -> torch.Tensor:

@@ -36,8 +36,33 @@ class FakeLibrary:
             return lambda *a, **k: None
         return getattr(N, name)
 
-    def workspace(self, shape, device):
-        return torch.zeros(8192, dtype=torch.uint8)
+    def workspace(self, shape, device):               # zero-filled, as the library's
+        return torch.zeros(self.moe_workspace_size(shape), dtype=torch.uint8)
+
+    def moe_workspace_size(self, shape):
+        return 8192 * shape.tokens
+
+    def moe_workspace_init(self, ws):
+        ws[:4096] = 0
+
+    # the device status: the workspace's first word
+    fails = ()                                        # (call, tokens) that raise one
+
+    def raised(self, call, shape, ws):
+        assert ws.nbytes >= self.moe_workspace_size(shape)
+        if (call, shape.tokens) in self.fails:
+            ws.view(torch.int32)[0] = N.MOE_ERR_NONFINITE
+
+    def moe_route(self, shape, *args):
+        self.raised("forward", shape, args[-1])
+
+    def moe_route_backward(self, shape, *args):
+        self.raised("backward", shape, args[-1])
+
+    def moe_status_read(self, ws):
+        status = int(ws.view(torch.int32)[0])
+        ws.view(torch.int32)[0] = 0
+        return status
 
     def layernorm_scratch(self, rows, hidden, device):
         return torch.zeros(1)
@@ -71,3 +96,38 @@ def test_a_graph_that_nothing_asks_for_does_not_matter(monkeypatch):
     b.zero_grad()
     b(x.detach()).float().sum().backward()
     assert all(not p.grad.requires_grad for p in b.parameters())
+
+
+@pytest.mark.parametrize("after", [2, 5, 9])
+def test_a_status_survives_other_batch_sizes(monkeypatch, after):
+    """An error of one batch is still there when check() comes after another one."""
+    fake = FakeLibrary()
+    monkeypatch.setattr(block_module, "N", fake)
+    b = block()
+    batch = lambda n: torch.zeros(n, 24, dtype=BF16, requires_grad=True)
+    b(batch(5))
+    b.check()
+    fake.fails = (("forward", 5),)
+    b(batch(5))
+    fake.fails = ()
+    b(batch(after))
+    with pytest.raises(N.MoEError) as e:
+        b.check()
+    assert e.value.status == N.MOE_ERR_NONFINITE
+    b.check()                                         # read and cleared
+    # an error of a backward pass that runs after another batch's forward
+    fake.fails = (("backward", 5),)
+    out = b(batch(5))
+    b(batch(after))
+    b.check()
+    out.float().sum().backward()
+    with pytest.raises(N.MoEError):
+        b.check()
+    # and the batch before is read with its own shape
+    fake.fails = ()
+    x = batch(7)
+    out = b(x)
+    b(batch(after))
+    out.float().sum().backward()
+    assert x.grad.shape == x.shape
+    b.check()

@@ -112,3 +112,28 @@ def test_block_refuses_other_inputs():
         block(torch.randn(3, 72, device=dev()).to(torch.bfloat16))
     with pytest.raises(N.MoEError):
         block(torch.empty(0, 64, device=dev(), dtype=torch.bfloat16))
+
+
+def test_batches_of_several_sizes_share_the_workspace():
+    """Gradients are those of each batch alone, bit for bit, whichever forward passes come
+    between, and an error of any of them waits for check()."""
+    gen = torch.Generator(device=dev()).manual_seed(5)
+    block = MoEBlock(136, 7, 3, 72, device=dev(), generator=gen)
+    sizes = [40, 513, 1, 300, 40]
+    xs = [torch.randn(n, 136, generator=gen, device=dev()).to(torch.bfloat16).requires_grad_() for n in sizes]
+    params = list(block.parameters())
+    alone = [torch.autograd.grad(block(x).float().square().sum(), [x, *params]) for x in xs]
+    outs = [block(x) for x in xs]
+    for out, x, want in reversed(list(zip(outs, xs, alone))):
+        got = torch.autograd.grad(out.float().square().sum(), [x, *params])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    block.check()
+    fresh = MoEBlock(136, 7, 3, 72, device=dev(), generator=gen)
+    nan = torch.full((40, 136), float("nan"), device=dev(), dtype=torch.bfloat16)
+    fresh(nan)
+    for n in (30, 2000):
+        fresh(torch.randn(n, 136, generator=gen, device=dev()).to(torch.bfloat16))
+    with pytest.raises(N.MoEError) as e:
+        fresh.check()
+    assert e.value.status == N.MOE_ERR_NONFINITE
+    fresh.check()
