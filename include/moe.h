@@ -363,7 +363,7 @@ MOE_API moe_status moe_ep_plan(int32_t experts, int32_t world, int32_t rank, int
  * gradients of each. The library's conventions hold: contiguous row-major buffers of the
  * caller, 16-byte aligned, work enqueued on `stream`, nothing allocated.  No
  * gradient is summed with atomics: results do not change from run to run.  The
- * gradient GEMMs may keep FP32 partial sums in the workspace (under 70 MB of
+ * gradient GEMMs may keep FP32 partial sums in the workspace (at most 70 MB of
  * moe_workspace_size), so calls that may overlap need a workspace each. */
 
 /* Layer norm over rows of `hidden` elements (any width from 1 to 2^20):

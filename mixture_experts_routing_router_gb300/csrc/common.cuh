@@ -54,6 +54,7 @@ struct GradDims {
 struct GradPlan { int r, w; };
 constexpr int kGradTile = 256, kGradStep = 64, kGradPairs = 76;   // output tile, reduction step, CTA pairs
 constexpr int kGradMinSteps = 8;      // of a part: a ring's worth
+constexpr long long kGradPartialBytes = 70000000 / kAlign * kAlign;    // most of a call's partial results (moe.h)
 inline GradPlan grad_plan(const GradDims& d) {
     auto tiles = [](long long n) { return (n + kGradTile - 1) / kGradTile; };
     const long long used = d.rows < d.groups ? d.rows : d.groups;
@@ -70,8 +71,16 @@ inline GradPlan grad_plan(const GradDims& d) {
     if (share < kGradMinSteps) share = kGradMinSteps;
     const long long unit = share / 3 > kGradMinSteps ? share / 3 : kGradMinSteps;
     auto parts = [&](long long n, long long k) { return n < 1 || k <= share + 20 ? 1LL : (k + unit / 2) / unit; };
-    const long long r = parts(rt, kr), w = parts(wt, kw);
-    return {(int)(r > 16 ? 16 : r), (int)(w > 16 ? 16 : w)};
+    long long r = parts(rt, kr), w = parts(wt, kw);
+    r = r > 16 ? 16 : r;
+    w = w > 16 ? 16 : w;
+    // fewer parts where their results would not fit: of the form that holds more
+    const long long r_one = d.rows * d.N * 4, w_one = (long long)d.groups * d.wM * d.wN * 4;      // bytes of a part
+    for (;;) {
+        const long long rb = r > 1 ? r * r_one : 0, wb = w > 1 ? w * w_one : 0;
+        if (rb + wb <= kGradPartialBytes) return {(int)r, (int)w};
+        --(rb > wb ? r : w);
+    }
 }
 // Floats of the rows form's and of both forms' partial results.
 inline size_t grad_rows_partials(const GradDims& d, const GradPlan& n) { return n.r > 1 ? (size_t)n.r * d.rows * d.N : 0; }
