@@ -102,6 +102,10 @@ typedef struct moe_shape {
  * moe_layer figure, which covers the others).  Host only, synchronous. */
 MOE_API moe_status moe_workspace_size(const moe_shape* shape, size_t* bytes);
 
+/* The same without what only moe_layer and its quantized forms keep there (x_perm, h,
+ * y_perm of the whole layer): enough for every other call with this shape. */
+MOE_API moe_status moe_workspace_stage_size(const moe_shape* shape, size_t* bytes);
+
 /* Zero the workspace's status word and counters.  Call once after allocating
  * a workspace (or allocate it zero-filled).  Enqueued on `stream`.
  * They are in its first 4096 bytes, all that stays in it between calls: a

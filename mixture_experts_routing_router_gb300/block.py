@@ -132,7 +132,7 @@ class MoEBlock(torch.nn.Module):
         The larger one takes over the header, so a status not yet read stays to be read."""
         if self._shape is None or self._shape.tokens != tokens:
             shape = N.make_shape(tokens, self.hidden, self.experts, self.top_k, self.inter, self.act)
-            self._bytes = N.moe_workspace_size(shape)
+            self._bytes = N.moe_workspace_stage_size(shape)
             self._shape = shape
         old = self._ws
         if old is None or old.device != device or old.nbytes < self._bytes:

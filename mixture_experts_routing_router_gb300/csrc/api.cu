@@ -347,6 +347,15 @@ moe_status moe_workspace_size(const moe_shape* shape, size_t* bytes) {
     return MOE_OK;
 }
 
+moe_status moe_workspace_stage_size(const moe_shape* shape, size_t* bytes) {
+    clear_error();
+    moe_status r = check_shape(shape);
+    if (r != MOE_OK) return r;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = ws_layout(*shape).stage_end;
+    return MOE_OK;
+}
+
 moe_status moe_workspace_init(void* ws, size_t ws_bytes, void* stream) {
     if (!aligned(ws, 256) || ws_bytes < 4096) return MOE_ERR_INVALID_ARG;
     return from_cuda(cudaMemsetAsync(ws, 0, 4096, static_cast<cudaStream_t>(stream)));

@@ -45,7 +45,7 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_dispatc
            "moe_timeout_site_read", "moe_ep_plan", "moe_layernorm", "moe_layernorm_scratch_size",
            "moe_layernorm_backward", "moe_combine_backward", "moe_dispatch_backward", "moe_route_backward",
            "moe_route_sigmoid_backward", "moe_gate_backward", "moe_expert_up_train", "moe_expert_down_backward",
-           "moe_expert_up_backward")
+           "moe_expert_up_backward", "moe_workspace_stage_size")
 
 
 class MoEError(RuntimeError):
@@ -92,6 +92,7 @@ def lib():
             I32, I64 = ctypes.c_int32, ctypes.c_int64
             sig = {
                 "moe_workspace_size": [SP, ctypes.POINTER(ctypes.c_size_t)],
+                "moe_workspace_stage_size": [SP, ctypes.POINTER(ctypes.c_size_t)],
                 "moe_workspace_init": [P, S, P],
                 "moe_route": [SP, P, P, P, P, S, P],
                 "moe_dispatch": [SP, P, P, P, P, P, P, P, P, S, P],
@@ -181,6 +182,13 @@ def _check(st, where):
 def moe_workspace_size(shape: moe_shape) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().moe_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "moe_workspace_size")
+    return n.value
+
+
+def moe_workspace_stage_size(shape: moe_shape) -> int:
+    """Bytes of workspace that every call but the whole-layer ones needs."""
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_workspace_stage_size(ctypes.byref(shape), ctypes.byref(n)), "moe_workspace_stage_size")
     return n.value
 
 

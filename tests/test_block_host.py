@@ -40,6 +40,9 @@ class FakeLibrary:
         return torch.zeros(self.moe_workspace_size(shape), dtype=torch.uint8)
 
     def moe_workspace_size(self, shape):
+        return 2 * self.moe_workspace_stage_size(shape)
+
+    def moe_workspace_stage_size(self, shape):
         return 8192 * shape.tokens
 
     def moe_workspace_init(self, ws):
@@ -49,7 +52,7 @@ class FakeLibrary:
     fails = ()                                        # (call, tokens) that raise one
 
     def raised(self, call, shape, ws):
-        assert ws.nbytes >= self.moe_workspace_size(shape)
+        assert ws.nbytes >= self.moe_workspace_stage_size(shape)
         if (call, shape.tokens) in self.fails:
             ws.view(torch.int32)[0] = N.MOE_ERR_NONFINITE
 
@@ -131,3 +134,14 @@ def test_a_status_survives_other_batch_sizes(monkeypatch, after):
     out.float().sum().backward()
     assert x.grad.shape == x.shape
     b.check()
+
+
+def test_the_workspace_is_that_of_the_calls_it_makes(monkeypatch):
+    """Not moe_layer's, which holds x_perm, h and y_perm a second time; and it only grows."""
+    fake = FakeLibrary()
+    monkeypatch.setattr(block_module, "N", fake)
+    b = block()
+    size = lambda n: fake.moe_workspace_stage_size(N.make_shape(n, 24, 4, 2, 8))
+    for n, want in ((5, 5), (3, 5), (9, 9), (5, 9)):
+        b(torch.zeros(n, 24, dtype=BF16))
+        assert b._ws.nbytes == size(want)

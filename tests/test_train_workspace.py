@@ -49,3 +49,26 @@ def test_partial_sums_stay_within_the_stated_size():
         assert 0 <= b <= LIMIT, (T, H, E, k, I)
         most = max(most, b)
     assert most > LIMIT // 2            # the draws reach the shapes that matter
+
+
+def test_stage_size():
+    """What the calls on their own need: none of moe_layer's x_perm, h and y_perm, 4.3 GB at
+    16384 tokens, k = 8, 7168 hidden."""
+    for act in (N.MOE_ACT_SWIGLU, N.MOE_ACT_RELU2):
+        s = N.make_shape(16384, 7168, 256, 8, 2048, act=act)
+        whole, stage = N.moe_workspace_size(s), N.moe_workspace_stage_size(s)
+        assert whole - stage > 2 * 16384 * 8 * 2 * 7168 and 4096 < stage < 100_000_000
+    with pytest.raises(N.MoEError):
+        N.moe_workspace_stage_size(N.make_shape(0, 64, 4, 2, 64))
+
+
+def test_stage_size_is_what_the_stage_calls_ask_for():
+    """One byte less is refused on the host, before anything is launched (the pointers are
+    never followed: the second refusal is that of a null output)."""
+    import ctypes
+    L, P = N.lib(), ctypes.c_void_p
+    s = N.make_shape(300, 136, 5, 2, 72)
+    n = N.moe_workspace_stage_size(s)
+    for bytes_, out in ((n - 1, P(4096)), (n, None)):
+        assert L.moe_expert_down_backward(ctypes.byref(s), P(4096), P(4096), P(4096), P(4096), P(4096), out, None, 0,
+                                          P(1 << 20), bytes_, None) == N.MOE_ERR_INVALID_ARG
