@@ -8,8 +8,10 @@ loaded, ``lib()`` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -401,104 +403,136 @@ def _arg(t, dtype, n, what):
     return _ptr(t)
 
 
-def _up(shape):
-    return 2 * shape.inter if shape.act == MOE_ACT_SWIGLU else shape.inter
+class _Counts(NamedTuple):
+    """Elements of the training calls' tensors."""
+    x: int          # [T, H]
+    pairs: int      # [T, k]
+    rows: int       # [T*k, H]
+    logits: int     # [T, E]
+    logits8: int    # [T, 8 * ceil(E / 8)]
+    bounds: int     # [E + 1]
+    pre: int        # [T*k, up]
+    h: int          # [T*k, I]
+    w_gate: int     # [E, H]
+    w13: int        # [E, up, H]
+    w2: int         # [E, H, I]
+
+
+@functools.lru_cache(maxsize=256)
+def _counts_of(fields: bytes) -> _Counts:
+    s = moe_shape.from_buffer_copy(fields)
+    T, H, E, I, R = s.tokens, s.hidden, s.experts, s.inter, s.tokens * s.top_k
+    up = 2 * I if s.act == MOE_ACT_SWIGLU else I
+    return _Counts(T * H, R, R * H, T * E, T * ((E + 7) // 8 * 8), E + 1, R * up, R * I, E * H, E * up * H, E * H * I)
 
 
 def moe_combine_backward(shape, dout, y_perm, dest, topk_w, dy_perm, dtopk_w, ws, stream=None):
     """Gradient of moe_combine: dy_perm, and dtopk_w unless it is None."""
-    T, H = shape.tokens, shape.hidden
-    R = T * shape.top_k
-    _check(lib().moe_combine_backward(ctypes.byref(shape), _arg(dout, _BF16, T * H, "dout"),
-                                      _arg(y_perm, _BF16, R * H, "y_perm"), _arg(dest, _I32, R, "dest"),
-                                      _arg(topk_w, _F32, R, "topk_w"), _arg(dy_perm, _BF16, R * H, "dy_perm"),
-                                      _arg(dtopk_w, _F32, R, "dtopk_w"), _ptr(ws), _wsb(ws), _stream(stream)),
-           "moe_combine_backward")
+    n = _counts_of(bytes(shape))
+    st = (_lib or lib()).moe_combine_backward(shape, _arg(dout, _BF16, n.x, "dout"),
+                                              _arg(y_perm, _BF16, n.rows, "y_perm"),
+                                              _arg(dest, _I32, n.pairs, "dest"),
+                                              _arg(topk_w, _F32, n.pairs, "topk_w"),
+                                              _arg(dy_perm, _BF16, n.rows, "dy_perm"),
+                                              _arg(dtopk_w, _F32, n.pairs, "dtopk_w"), _ptr(ws), _wsb(ws),
+                                              _stream(stream))
+    if st:
+        raise MoEError(st, "moe_combine_backward")
 
 
 def moe_dispatch_backward(shape, dx_perm, dest, dx, ws, stream=None, add=None):
     """Gradient of moe_dispatch's row copy, plus `add`."""
-    T, H = shape.tokens, shape.hidden
-    R = T * shape.top_k
-    _check(lib().moe_dispatch_backward(ctypes.byref(shape), _arg(dx_perm, _BF16, R * H, "dx_perm"),
-                                       _arg(dest, _I32, R, "dest"), _arg(add, _BF16, T * H, "add"),
-                                       _arg(dx, _BF16, T * H, "dx"), _ptr(ws), _wsb(ws), _stream(stream)),
-           "moe_dispatch_backward")
+    n = _counts_of(bytes(shape))
+    st = (_lib or lib()).moe_dispatch_backward(shape, _arg(dx_perm, _BF16, n.rows, "dx_perm"),
+                                               _arg(dest, _I32, n.pairs, "dest"), _arg(add, _BF16, n.x, "add"),
+                                               _arg(dx, _BF16, n.x, "dx"), _ptr(ws), _wsb(ws), _stream(stream))
+    if st:
+        raise MoEError(st, "moe_dispatch_backward")
 
 
 def moe_route_backward(shape, topk_ids, topk_w, dtopk_w, dlogits, ws, stream=None):
-    T = shape.tokens
-    R = T * shape.top_k
-    _check(lib().moe_route_backward(ctypes.byref(shape), _arg(topk_ids, _I32, R, "topk_ids"),
-                                    _arg(topk_w, _F32, R, "topk_w"), _arg(dtopk_w, _F32, R, "dtopk_w"),
-                                    _arg(dlogits, _F32, T * shape.experts, "dlogits"), _ptr(ws), _wsb(ws),
-                                    _stream(stream)), "moe_route_backward")
+    n = _counts_of(bytes(shape))
+    st = (_lib or lib()).moe_route_backward(shape, _arg(topk_ids, _I32, n.pairs, "topk_ids"),
+                                            _arg(topk_w, _F32, n.pairs, "topk_w"),
+                                            _arg(dtopk_w, _F32, n.pairs, "dtopk_w"),
+                                            _arg(dlogits, _F32, n.logits, "dlogits"), _ptr(ws), _wsb(ws),
+                                            _stream(stream))
+    if st:
+        raise MoEError(st, "moe_route_backward")
 
 
 def moe_route_sigmoid_backward(shape, logits, topk_ids, route_scale, dtopk_w, dlogits, ws, stream=None):
-    T, E = shape.tokens, shape.experts
-    R = T * shape.top_k
-    _check(lib().moe_route_sigmoid_backward(ctypes.byref(shape), _arg(logits, _F32, T * E, "logits"),
-                                            _arg(topk_ids, _I32, R, "topk_ids"), float(route_scale),
-                                            _arg(dtopk_w, _F32, R, "dtopk_w"), _arg(dlogits, _F32, T * E, "dlogits"),
-                                            _ptr(ws), _wsb(ws), _stream(stream)), "moe_route_sigmoid_backward")
+    n = _counts_of(bytes(shape))
+    st = (_lib or lib()).moe_route_sigmoid_backward(shape, _arg(logits, _F32, n.logits, "logits"),
+                                                    _arg(topk_ids, _I32, n.pairs, "topk_ids"), float(route_scale),
+                                                    _arg(dtopk_w, _F32, n.pairs, "dtopk_w"),
+                                                    _arg(dlogits, _F32, n.logits, "dlogits"), _ptr(ws), _wsb(ws),
+                                                    _stream(stream))
+    if st:
+        raise MoEError(st, "moe_route_sigmoid_backward")
 
 
 def _wgrad(dw, add):
     """The moe_wgrad value of a weight gradient's tensor."""
     if dw is None:
         return MOE_WGRAD_BF16
-    if _type(dw) == MOE_TYPE_F32:
+    if dw.dtype is _F32:
         return MOE_WGRAD_F32_ADD if add else MOE_WGRAD_F32
+    _type(dw)
     if add:
         raise ValueError("weight gradients are accumulated in float32")
     return MOE_WGRAD_BF16
 
 
-def _dw(dw, n, what):
-    """The address of a weight gradient of `n` elements, of either type `_wgrad` takes."""
-    return None if dw is None else _arg(dw, _F32 if dw.dtype is _F32 else _BF16, n, what)
-
-
 def moe_gate_backward(shape, dlogits, x, w_gate, dlogits_bf16, dx, dw_gate, ws, stream=None, add=False):
     """dx (None: skipped) and dw_gate (None: skipped; bfloat16 or float32, `add` accumulates into
     float32) from dlogits, rounded into dlogits_bf16 [T, 8 * ceil(E / 8)] on the way."""
-    T, H, E = shape.tokens, shape.hidden, shape.experts
-    _check(lib().moe_gate_backward(ctypes.byref(shape), _arg(dlogits, _F32, T * E, "dlogits"),
-                                   _arg(x, _BF16, T * H, "x"), _arg(w_gate, _BF16, E * H, "w_gate"),
-                                   _arg(dlogits_bf16, _BF16, T * ((E + 7) // 8 * 8), "dlogits_bf16"),
-                                   _arg(dx, _BF16, T * H, "dx"), _dw(dw_gate, E * H, "dw_gate"),
-                                   _wgrad(dw_gate, add), _ptr(ws), _wsb(ws), _stream(stream)), "moe_gate_backward")
+    n, mode = _counts_of(bytes(shape)), _wgrad(dw_gate, add)
+    st = (_lib or lib()).moe_gate_backward(shape, _arg(dlogits, _F32, n.logits, "dlogits"), _arg(x, _BF16, n.x, "x"),
+                                           _arg(w_gate, _BF16, n.w_gate, "w_gate"),
+                                           _arg(dlogits_bf16, _BF16, n.logits8, "dlogits_bf16"),
+                                           _arg(dx, _BF16, n.x, "dx"),
+                                           _arg(dw_gate, _F32 if mode else _BF16, n.w_gate, "dw_gate"), mode,
+                                           _ptr(ws), _wsb(ws), _stream(stream))
+    if st:
+        raise MoEError(st, "moe_gate_backward")
 
 
 def moe_expert_up_train(shape, x_perm, offsets, w13, pre, h, ws, stream=None):
     """Up projection that also keeps its pre-activations for the backward pass."""
-    R, H, E, I, up = shape.tokens * shape.top_k, shape.hidden, shape.experts, shape.inter, _up(shape)
-    _check(lib().moe_expert_up_train(ctypes.byref(shape), _arg(x_perm, _BF16, R * H, "x_perm"),
-                                     _arg(offsets, _I32, E + 1, "offsets"), _arg(w13, _BF16, E * up * H, "w13"),
-                                     _arg(pre, _BF16, R * up, "pre"), _arg(h, _BF16, R * I, "h"),
-                                     _ptr(ws), _wsb(ws), _stream(stream)), "moe_expert_up_train")
+    n = _counts_of(bytes(shape))
+    st = (_lib or lib()).moe_expert_up_train(shape, _arg(x_perm, _BF16, n.rows, "x_perm"),
+                                             _arg(offsets, _I32, n.bounds, "offsets"), _arg(w13, _BF16, n.w13, "w13"),
+                                             _arg(pre, _BF16, n.pre, "pre"), _arg(h, _BF16, n.h, "h"), _ptr(ws),
+                                             _wsb(ws), _stream(stream))
+    if st:
+        raise MoEError(st, "moe_expert_up_train")
 
 
 def moe_expert_down_backward(shape, dy_perm, offsets, w2, pre, h, dpre, dw2, ws, stream=None, add=False):
     """dpre (None: skipped) and dw2 (None: skipped; bfloat16 or float32, `add` accumulates into float32)."""
-    R, H, E, I, up = shape.tokens * shape.top_k, shape.hidden, shape.experts, shape.inter, _up(shape)
-    _check(lib().moe_expert_down_backward(ctypes.byref(shape), _arg(dy_perm, _BF16, R * H, "dy_perm"),
-                                          _arg(offsets, _I32, E + 1, "offsets"), _arg(w2, _BF16, E * H * I, "w2"),
-                                          _arg(pre, _BF16, R * up, "pre"), _arg(h, _BF16, R * I, "h"),
-                                          _arg(dpre, _BF16, R * up, "dpre"), _dw(dw2, E * H * I, "dw2"),
-                                          _wgrad(dw2, add), _ptr(ws), _wsb(ws), _stream(stream)),
-           "moe_expert_down_backward")
+    n, mode = _counts_of(bytes(shape)), _wgrad(dw2, add)
+    st = (_lib or lib()).moe_expert_down_backward(shape, _arg(dy_perm, _BF16, n.rows, "dy_perm"),
+                                                  _arg(offsets, _I32, n.bounds, "offsets"),
+                                                  _arg(w2, _BF16, n.w2, "w2"), _arg(pre, _BF16, n.pre, "pre"),
+                                                  _arg(h, _BF16, n.h, "h"), _arg(dpre, _BF16, n.pre, "dpre"),
+                                                  _arg(dw2, _F32 if mode else _BF16, n.w2, "dw2"), mode, _ptr(ws),
+                                                  _wsb(ws), _stream(stream))
+    if st:
+        raise MoEError(st, "moe_expert_down_backward")
 
 
 def moe_expert_up_backward(shape, dpre, offsets, x_perm, w13, dx_perm, dw13, ws, stream=None, add=False):
     """dx_perm (None: skipped) and dw13 (None: skipped; types as dw2)."""
-    R, H, E, up = shape.tokens * shape.top_k, shape.hidden, shape.experts, _up(shape)
-    _check(lib().moe_expert_up_backward(ctypes.byref(shape), _arg(dpre, _BF16, R * up, "dpre"),
-                                        _arg(offsets, _I32, E + 1, "offsets"), _arg(x_perm, _BF16, R * H, "x_perm"),
-                                        _arg(w13, _BF16, E * up * H, "w13"), _arg(dx_perm, _BF16, R * H, "dx_perm"),
-                                        _dw(dw13, E * up * H, "dw13"), _wgrad(dw13, add), _ptr(ws), _wsb(ws),
-                                        _stream(stream)), "moe_expert_up_backward")
+    n, mode = _counts_of(bytes(shape)), _wgrad(dw13, add)
+    st = (_lib or lib()).moe_expert_up_backward(shape, _arg(dpre, _BF16, n.pre, "dpre"),
+                                                _arg(offsets, _I32, n.bounds, "offsets"),
+                                                _arg(x_perm, _BF16, n.rows, "x_perm"), _arg(w13, _BF16, n.w13, "w13"),
+                                                _arg(dx_perm, _BF16, n.rows, "dx_perm"),
+                                                _arg(dw13, _F32 if mode else _BF16, n.w13, "dw13"), mode, _ptr(ws),
+                                                _wsb(ws), _stream(stream))
+    if st:
+        raise MoEError(st, "moe_expert_up_backward")
 
 
 def moe_ep_plan(experts: int, world: int, rank: int, capacity: int, counts_all):
