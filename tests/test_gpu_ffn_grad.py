@@ -395,3 +395,39 @@ def test_refused_bounds_leave_the_weight_gradient_of_empty_buckets(case, bad):
     dw2, dw13 = old2.clone(), old13.clone()
     calls(dw2, dw13, add=True)
     assert torch.equal(dw2, old2) and torch.equal(dw13, old13)
+
+
+def many_buckets(E, seed):
+    """Ragged and empty buckets, and two of several rounds of either ring plus a remainder."""
+    g = torch.Generator().manual_seed(seed)
+    sizes = torch.tensor([0, 0, 1, 2, 15, 16, 17, 33, 63, 64, 65, 100])
+    counts = sizes[torch.randint(0, len(sizes), (E,), generator=g)].tolist()
+    counts[E // 3], counts[E - 2] = 3 * 5 * 64 + 7, 2 * 6 * 64 + 60
+    return counts
+
+
+# around the change from six stages to five (up to 63 groups have room for six), up to the
+# most experts; from 353 on a thread counts several groups' tiles
+@pytest.mark.parametrize("E", [33, 63, 64, 65, 240, 352, 353, 705, 1024])
+@pytest.mark.parametrize("glu", [True, False], ids=["swiglu", "relu2"])
+def test_many_experts(E, glu):
+    counts = many_buckets(E, E)
+    c = Case(counts, 136 if E < 300 else 72, 72 if E < 300 else 40, glu, seed=E)
+    run_and_check(c, counts)
+    # each form alone: the same bits as together
+    a, b = (dict(dpre=torch.zeros_like(c.pre), dw2=torch.zeros_like(c.w2), dx=torch.zeros_like(c.x),
+                 dw13=torch.zeros_like(c.w13)) for _ in range(2))
+    N.moe_expert_down_backward(c.shape, c.dy, c.offsets, c.w2, c.pre, c.h, b["dpre"], b["dw2"], c.ws)
+    N.moe_expert_up_backward(c.shape, c.dpre_in, c.offsets, c.x, c.w13, b["dx"], b["dw13"], c.ws)
+    N.moe_expert_down_backward(c.shape, c.dy, c.offsets, c.w2, c.pre, None, a["dpre"], None, c.ws)
+    N.moe_expert_down_backward(c.shape, c.dy, c.offsets, None, None, c.h, None, a["dw2"], c.ws)
+    N.moe_expert_up_backward(c.shape, c.dpre_in, c.offsets, None, c.w13, a["dx"], None, c.ws)
+    N.moe_expert_up_backward(c.shape, c.dpre_in, c.offsets, c.x, None, None, a["dw13"], c.ws)
+    c.status()
+    assert all(torch.equal(a[n].view(torch.int16), b[n].view(torch.int16)) for n in a)
+
+
+@pytest.mark.parametrize("E", [63, 64, 65])
+def test_split_reductions_of_many_experts(E):
+    """Few rows an expert and a long reduction: the rows form split in either ring."""
+    run_and_check(Case([1 + e % 2 for e in range(E)], 9216, 8, E % 2 == 0, seed=E), [2])
