@@ -9,7 +9,8 @@ moe_combine_backward, moe_route_backward, moe_expert_down_backward,
 moe_expert_up_backward, moe_gate_backward, moe_dispatch_backward (the gate's part
 of dn added there) and moe_layernorm_backward (the residual's gradient added
 there).  torch carries memory, streams and the autograd graph; every number comes
-from the library's kernels.
+from the library's kernels.  dn is rounded twice: the gate's part to BF16 (g w_gate), then
+its sum with the experts' part.
 
 Reference: DeepSeek fleet megakernel REPORT.md, the per-op table (MOE_GATE_TOPK,
 EXPERT_W13_SILU, EXPERT_W2, MOE_COMBINE_RESIDUAL) for the block's forward chain.
