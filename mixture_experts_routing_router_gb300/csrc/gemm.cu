@@ -1092,8 +1092,9 @@ grouped_gemm_q_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
         bool ok = true;
         for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
             for (int i = 0; i < nk; ++i) {
-                if (!mbar_wait_warp(smem_u32(&ctl->full[stage]), ph, abort) ||
-                    !mbar_wait_warp(smem_u32(&ctl->cempty[cs]), cph ^ 1u, abort)) { ok = false; break; }
+                // voted on where the step ends (a lane that gave up converts what is there)
+                const bool landed = mbar_wait_bounded(smem_u32(&ctl->full[stage]), ph, abort) &&
+                                    mbar_wait_bounded(smem_u32(&ctl->cempty[cs]), cph ^ 1u, abort);
                 const uint8_t* codes = smem + stage * QG::STAGE_BYTES + A_BYTES;
                 // NVFP4: this quarter's block scale of each pass, from the stage (0x100
                 // marks a block past K: zeros; rows past the weights arrive as scale 0)
@@ -1142,6 +1143,7 @@ grouped_gemm_q_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 // the BF16 tile is read by the tensor core (async proxy); the codes
                 // have been read: release both
                 fence_proxy_async_smem();
+                if (!__all_sync(0xffffffffu, landed)) { ok = false; break; }
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&ctl->cfull[cs]));

@@ -73,13 +73,20 @@ KERNELS_THAT_WAIT = ["gemm.cu", "gemm_decode.cu", "decode_ffn.cu", "gemm_grad.cu
 def test_a_warp_gives_up_a_wait_as_a_whole(name):
     """Lanes that decide apart whether a wait ran out part for good: some reach the
     closing barrier, the rest a warp-wide instruction, and both wait for ever.  A wait
-    outside a block of one thread has to be the warp's."""
+    outside a block of one thread has to be the warp's, or its verdict `landed` has to be
+    voted on before anything else of the warp and before anyone leaves."""
     waits = 0
     for kernel, body in kernels(name):
         for m in re.finditer(r"\b(mbar_wait_bounded|mbar_wait_cluster|drain_ring|wait_armed_stages)\(", body):
             waits += 1
-            assert any(SINGLE.search(h) for h in enclosing(body, m.start())), \
+            if any(SINGLE.search(h) for h in enclosing(body, m.start())):
+                continue
+            statement = body[:m.start()].rsplit(";", 1)[-1].rsplit("{", 1)[-1].rsplit("}", 1)[-1]
+            assert re.match(r"\s*(const )?(bool )?landed = ", statement), \
                 f"{kernel}: {body[m.start():m.start() + 70]!r}"
+            between, vote, _ = body[m.start():].partition("if (!__all_sync(0xffffffffu, landed)) { ok = false; break; }")
+            assert vote, kernel
+            assert not re.search(r"\b(break|continue|return|goto)\b|_sync\b|tmem_|__syncwarp|__syncthreads", between), kernel
     assert waits > 4
 
 
