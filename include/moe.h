@@ -78,6 +78,29 @@ typedef enum moe_wgrad {
     MOE_WGRAD_F32_ADD = 2  /* dw += sum, FP32: gradient accumulation */
 } moe_wgrad;
 
+/* How a router turns logits into scores. */
+typedef enum moe_score {
+    MOE_SCORE_SOFTMAX = 0,   /* over all experts of the token */
+    MOE_SCORE_SIGMOID = 1
+} moe_score;
+
+/* Group-limited routing (moe_route_grouped).
+ *   score        a moe_score value
+ *   groups       G, 1 to 32, divides the experts: group g holds experts
+ *                [g E / G, (g + 1) E / G); 1: no limit
+ *   topk_groups  groups a token may use, 1 to G, with top_k experts in them at least
+ *   group_top    1: a group is worth its largest key; 2: the sum of its two largest
+ *   renorm       1: the weights of a token sum to `scale`; 0: scale times the score
+ *   scale        finite */
+typedef struct moe_router {
+    int32_t score;
+    int32_t groups;
+    int32_t topk_groups;
+    int32_t group_top;
+    int32_t renorm;
+    float scale;
+} moe_router;
+
 /* Shape of one layer call.
  *   tokens T >= 1; hidden H, multiple of 8; experts E in [1, 1024];
  *   top_k k in [1, min(E, 32)]; inter I, multiple of 8 (expert intermediate);
@@ -148,6 +171,24 @@ MOE_API moe_status moe_gate(const moe_shape* shape, const uint16_t* x, const uin
 MOE_API moe_status moe_route_sigmoid(const moe_shape* shape, const float* logits, const float* bias,
                                      float route_scale, int32_t* topk_ids, float* topk_w, void* ws,
                                      size_t ws_bytes, void* stream);
+
+/* Group-limited routing (the scores, bias and mixture weights of ONNX Runtime PR
+ * #33963, Description bullet 2, with the choice limited to a token's best groups of
+ * experts).  Per token: s_e = sigmoid(logit_e) or softmax over all E, taken in double
+ * and rounded once to FP32; key_e = s_e + bias[e] in FP32; a group's value is its
+ * largest key or the FP32 sum of its two largest; of the topk_groups groups of the
+ * largest value the k experts of the largest keys are selected, in descending key
+ * order, ties to the lower index throughout.  topk_w[t,j] = scale * s, divided by the
+ * sum over the selection when renorm is 1 (FP32; from the logits, so scores that all
+ * underflow keep their ratios).
+ *   logits device f32 [T, E]; bias device f32 [E] (4-byte aligned) or NULL;
+ *   topk_ids device i32 [T, k] out; topk_w device f32 [T, k] out.
+ * With one group and sigmoid scores the ids are those of moe_route_sigmoid.
+ * Device error: MOE_ERR_NONFINITE if a logit or a bias is NaN or infinite.
+ * moe_route_grouped_backward is its gradient (Training, below). */
+MOE_API moe_status moe_route_grouped(const moe_shape* shape, const moe_router* router, const float* logits,
+                                     const float* bias, int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes,
+                                     void* stream);
 
 /* Count-first dispatch (afdEP-comm count-first record, .change: per-expert
  * counts and their prefix sums come before the payload rows move).
@@ -300,6 +341,55 @@ MOE_API moe_status moe_layer_nvfp4(const moe_shape* shape, const float* logits, 
                                    const uint8_t* w2_bscale, const float* w2_scale, const uint16_t* residual,
                                    uint16_t* out, void* ws, size_t ws_bytes, void* stream);
 
+/* Experts in block-scaled FP8: activations and weights both E4M3 (OCP), multiplied on
+ * the FP8 tensor cores, with FP32 scales per block of 128 (the afdEP-comm record's fp8
+ * payload, its values scaled by blocks).  With nb(n) = ceil(n / 128):
+ *   activation rows  codes u8 [rows, n], scale f32 [rows, nb(n)]: the value is
+ *                    code * scale[r][c / 128]
+ *   weights          codes u8 [N, K], scale f32 [nb(N), nb(K)]: the value is
+ *                    code * scale[n / 128][k / 128].  w13 is [E, P, I, H] with scales
+ *                    [E, P, nb(I), nb(H)], P = 2 for SwiGLU (gate, then up, each with
+ *                    blocks of its own) and 1 for ReLU^2; w2 [E, H, I], [E, nb(H), nb(I)].
+ * Rows are quantized by the library: for a block of a row with a = max(max|x|, 2^-100),
+ * scale = a / 448 and code = the E4M3 value nearest 448 x / a (ties to even); a block
+ * with a NaN or an infinity gets NaN codes and a NaN scale, and its row's outputs are NaN.
+ * NaN codes in the weights make the outputs that they reach NaN.
+ * Sums are FP32: each 128-wide block's sum of products, times both scales, added up.
+ * A row's results do not depend on which rows share its call or its bucket.
+ * Host errors: MOE_ERR_UNSUPPORTED when shape->shared > 0; MOE_ERR_INVALID_ARG when
+ * hidden or inter is not a multiple of 16 or a pointer is not 16-byte aligned.
+ * For serving: these weights have no gradient calls. */
+
+/* moe_dispatch with the rows quantized on the way:
+ *   x       device bf16 [T, H]
+ *   x_perm  device u8 [T*k, H], x_scale device f32 [T*k, nb(H)]  out: row dest[p] is x[p / k]
+ * The other arguments, the placement and the device errors are those of moe_dispatch. */
+MOE_API moe_status moe_dispatch_fp8_block(const moe_shape* shape, const uint16_t* x, const int32_t* topk_ids,
+                                          int32_t* counts, int32_t* offsets, int32_t* dest, int32_t* sorted_pair,
+                                          uint8_t* x_perm, float* x_scale, void* ws, size_t ws_bytes, void* stream);
+
+/* Up projection, activation and quantization of its result:
+ *   h device u8 [T*k, I], h_scale device f32 [T*k, nb(I)]  out: act(x_perm W13[e]^T),
+ *     rows past offsets[E] not written. */
+MOE_API moe_status moe_expert_up_fp8_block(const moe_shape* shape, const uint8_t* x_perm, const float* x_scale,
+                                           const int32_t* offsets, const uint8_t* w13, const float* w13_scale,
+                                           uint8_t* h, float* h_scale, void* ws, size_t ws_bytes, void* stream);
+
+/* Down projection: y_perm device bf16 [T*k, H] out = bf16(h W2[e]^T), rows past
+ * offsets[E] not written. */
+MOE_API moe_status moe_expert_down_fp8_block(const moe_shape* shape, const uint8_t* h, const float* h_scale,
+                                             const int32_t* offsets, const uint8_t* w2, const float* w2_scale,
+                                             uint16_t* y_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_layer on these experts: route (softmax top-k of logits) or preselected ids and
+ * weights (those of moe_route_grouped, say), then the three calls above and moe_combine,
+ * with every intermediate in the workspace; the same bits as the calls one by one. */
+MOE_API moe_status moe_layer_fp8_block(const moe_shape* shape, const float* logits, const int32_t* ids_in,
+                                       const float* w_in, const uint16_t* x, const uint8_t* w13,
+                                       const float* w13_scale, const uint8_t* w2, const float* w2_scale,
+                                       const uint16_t* residual, uint16_t* out, void* ws, size_t ws_bytes,
+                                       void* stream);
+
 /* moe_dispatch for callers that cannot allocate device memory, and so cannot
  * provide the workspace the other calls take: code that runs where cudaMalloc
  * is not allowed or not safe (while a CUDA graph is being captured, inside a
@@ -435,6 +525,18 @@ MOE_API moe_status moe_route_backward(const moe_shape* shape, const int32_t* top
  * call; device errors as moe_route_backward. */
 MOE_API moe_status moe_route_sigmoid_backward(const moe_shape* shape, const float* logits, const int32_t* topk_ids,
                                               float route_scale, const float* dtopk_w, float* dlogits, void* ws,
+                                              size_t ws_bytes, void* stream);
+
+/* Gradient of moe_route_grouped for the selection topk_ids (the bias and the groups only
+ * select).  With s the scores, p_j = s_j / sum_i s_i over the selection, g = dtopk_w:
+ *   softmax, renorm  dlogits[ids[j]] = scale p_j (g_j - sum_i p_i g_i), 0 elsewhere
+ *   softmax          dlogits[e] = scale s_e ([e selected] g_e - sum_i s_i g_i), every expert
+ *   sigmoid, renorm  dlogits[ids[j]] = scale p_j (1 - s_j) (g_j - sum_i p_i g_i), 0 elsewhere
+ *   sigmoid          dlogits[ids[j]] = scale s_j (1 - s_j) g_j, 0 elsewhere
+ * logits, topk_ids, router as in the forward call; dlogits device f32 [T, E] out.
+ * Device errors as moe_route_backward. */
+MOE_API moe_status moe_route_grouped_backward(const moe_shape* shape, const moe_router* router, const float* logits,
+                                              const int32_t* topk_ids, const float* dtopk_w, float* dlogits, void* ws,
                                               size_t ws_bytes, void* stream);
 
 /* Gradient of moe_gate:

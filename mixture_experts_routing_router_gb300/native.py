@@ -38,6 +38,9 @@ MOE_WGRAD_BF16 = 0
 MOE_WGRAD_F32 = 1
 MOE_WGRAD_F32_ADD = 2
 
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+
 # every symbol include/moe.h declares
 EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_dispatch", "moe_expert_up",
            "moe_expert_down", "moe_expert_ffn", "moe_combine", "moe_layer", "moe_status_read",
@@ -47,7 +50,8 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_dispatc
            "moe_timeout_site_read", "moe_ep_plan", "moe_layernorm", "moe_layernorm_scratch_size",
            "moe_layernorm_backward", "moe_combine_backward", "moe_dispatch_backward", "moe_route_backward",
            "moe_route_sigmoid_backward", "moe_gate_backward", "moe_expert_up_train", "moe_expert_down_backward",
-           "moe_expert_up_backward", "moe_workspace_stage_size")
+           "moe_expert_up_backward", "moe_workspace_stage_size", "moe_route_grouped", "moe_route_grouped_backward",
+           "moe_dispatch_fp8_block", "moe_expert_up_fp8_block", "moe_expert_down_fp8_block", "moe_layer_fp8_block")
 
 
 class MoEError(RuntimeError):
@@ -67,6 +71,16 @@ def make_shape(tokens, hidden, experts, top_k, inter, act=MOE_ACT_SWIGLU, shared
                capacity=0) -> moe_shape:
     return moe_shape(tokens, hidden, experts, top_k, inter, shared, shared_inter,
                      capacity if capacity > 0 else tokens, act)
+
+
+class moe_router(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+def make_router(score=MOE_SCORE_SIGMOID, groups=1, topk_groups=1, group_top=2, renorm=True, scale=1.0) -> moe_router:
+    """The description of a group-limited router (moe_route_grouped)."""
+    return moe_router(score, groups, topk_groups, group_top, int(renorm), scale)
 
 
 def shape_of(wl) -> moe_shape:
@@ -90,7 +104,7 @@ def lib():
                                    "(nvcc, sm_103a); there is no CPU fallback")
             L = ctypes.CDLL(LIB_PATH)
             P, S = ctypes.c_void_p, ctypes.c_size_t
-            SP = ctypes.POINTER(moe_shape)
+            SP, RP = ctypes.POINTER(moe_shape), ctypes.POINTER(moe_router)
             I32, I64 = ctypes.c_int32, ctypes.c_int64
             sig = {
                 "moe_workspace_size": [SP, ctypes.POINTER(ctypes.c_size_t)],
@@ -127,6 +141,12 @@ def lib():
                 "moe_expert_up_train": [SP, P, P, P, P, P, P, S, P],
                 "moe_expert_down_backward": [SP, P, P, P, P, P, P, P, I32, P, S, P],
                 "moe_expert_up_backward": [SP, P, P, P, P, P, P, I32, P, S, P],
+                "moe_route_grouped": [SP, RP, P, P, P, P, P, S, P],
+                "moe_route_grouped_backward": [SP, RP, P, P, P, P, P, S, P],
+                "moe_dispatch_fp8_block": [SP, P, P, P, P, P, P, P, P, P, S, P],
+                "moe_expert_up_fp8_block": [SP, P, P, P, P, P, P, P, P, S, P],
+                "moe_expert_down_fp8_block": [SP, P, P, P, P, P, P, P, S, P],
+                "moe_layer_fp8_block": [SP, P, P, P, P, P, P, P, P, P, P, P, S, P],
             }
             for name, args in sig.items():
                 fn = getattr(L, name)
@@ -533,6 +553,135 @@ def moe_expert_up_backward(shape, dpre, offsets, x_perm, w13, dx_perm, dw13, ws,
                                                 _wsb(ws), _stream(stream))
     if st:
         raise MoEError(st, "moe_expert_up_backward")
+
+
+# ---- group-limited routing, block-scaled FP8 experts -------------------------
+FP8_BLOCK = 128
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def fp8_blocks(n: int) -> int:
+    """Scales of n columns (or of n weight rows)."""
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def _on(t, dtypes, n, what):
+    """The address of a contiguous tensor of the current device with `n` elements at least of
+    one of `dtypes`; None and plain addresses pass as they are."""
+    try:
+        if t.dtype in dtypes and t.numel() >= n and t.is_cuda and t.is_contiguous() and \
+                t.get_device() == torch._C._cuda_getDevice():
+            return t.data_ptr()
+    except AttributeError:
+        return _ptr(t)
+    if t.dtype not in dtypes or t.numel() < n:
+        raise ValueError(f"{what}: {' or '.join(map(str, dtypes))} with {n} elements at least expected, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    p = _ptr(t)
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{what}: a tensor of {t.device}, the current device is {torch._C._cuda_getDevice()}")
+    return p
+
+
+_B, _F, _I, _C, _U = (_BF16,), (_F32,), (_I32,), _CODES, (torch.uint8,)
+
+
+class _Fp8Counts(NamedTuple):
+    """Elements of the block-scaled calls' tensors."""
+    x_perm: int     # [T*k, H]
+    x_scale: int    # [T*k, nb(H)]
+    w13: int        # [E, P, I, H]
+    w13_scale: int  # [E, P, nb(I), nb(H)]
+    h: int          # [T*k, I]
+    h_scale: int    # [T*k, nb(I)]
+    w2: int         # [E, H, I]
+    w2_scale: int   # [E, nb(H), nb(I)]
+
+
+@functools.lru_cache(maxsize=256)
+def _fp8_counts(fields: bytes) -> _Fp8Counts:
+    s = moe_shape.from_buffer_copy(fields)
+    H, E, I, R = s.hidden, s.experts, s.inter, s.tokens * s.top_k
+    P, bh, bi = 2 if s.act == MOE_ACT_SWIGLU else 1, fp8_blocks(s.hidden), fp8_blocks(s.inter)
+    return _Fp8Counts(R * H, R * bh, E * P * I * H, E * P * bi * bh, R * I, R * bi, E * H * I, E * bh * bi)
+
+
+def moe_route_grouped(shape, router, logits, bias, topk_ids, topk_w, ws, stream=None):
+    """Group-limited top-k routing of float32 logits; `bias` (or None) only selects."""
+    n = _counts_of(bytes(shape))
+    st = (_lib or lib()).moe_route_grouped(shape, router, _on(logits, _F, n.logits, "logits"),
+                                           _on(bias, _F, shape.experts, "bias"),
+                                           _on(topk_ids, _I, n.pairs, "topk_ids"), _on(topk_w, _F, n.pairs, "topk_w"),
+                                           _on(ws, _U, 0, "ws"), _wsb(ws), _stream(stream))
+    if st:
+        raise MoEError(st, "moe_route_grouped")
+
+
+def moe_route_grouped_backward(shape, router, logits, topk_ids, dtopk_w, dlogits, ws, stream=None):
+    """Gradient of moe_route_grouped's weights in the logits, for the selection topk_ids."""
+    n = _counts_of(bytes(shape))
+    st = (_lib or lib()).moe_route_grouped_backward(shape, router, _on(logits, _F, n.logits, "logits"),
+                                                    _on(topk_ids, _I, n.pairs, "topk_ids"),
+                                                    _on(dtopk_w, _F, n.pairs, "dtopk_w"),
+                                                    _on(dlogits, _F, n.logits, "dlogits"), _on(ws, _U, 0, "ws"),
+                                                    _wsb(ws), _stream(stream))
+    if st:
+        raise MoEError(st, "moe_route_grouped_backward")
+
+
+def moe_dispatch_fp8_block(shape, x, topk_ids, counts, offsets, dest, sorted_pair, x_perm, x_scale, ws, stream=None):
+    """moe_dispatch with the rows quantized: x_perm E4M3 codes (uint8 or float8_e4m3fn) [T*k, H],
+    x_scale float32 [T*k, ceil(H / 128)]."""
+    n, m = _counts_of(bytes(shape)), _fp8_counts(bytes(shape))
+    st = (_lib or lib()).moe_dispatch_fp8_block(shape, _on(x, _B, n.x, "x"), _on(topk_ids, _I, n.pairs, "topk_ids"),
+                                                _on(counts, _I, shape.experts, "counts"),
+                                                _on(offsets, _I, n.bounds, "offsets"), _on(dest, _I, n.pairs, "dest"),
+                                                _on(sorted_pair, _I, n.pairs, "sorted_pair"),
+                                                _on(x_perm, _C, m.x_perm, "x_perm"),
+                                                _on(x_scale, _F, m.x_scale, "x_scale"), _on(ws, _U, 0, "ws"), _wsb(ws),
+                                                _stream(stream))
+    if st:
+        raise MoEError(st, "moe_dispatch_fp8_block")
+
+
+def moe_expert_up_fp8_block(shape, x_perm, x_scale, offsets, w13, w13_scale, h, h_scale, ws, stream=None):
+    """Up projection and activation in block-scaled FP8, quantized again into h and h_scale."""
+    n, m = _counts_of(bytes(shape)), _fp8_counts(bytes(shape))
+    st = (_lib or lib()).moe_expert_up_fp8_block(shape, _on(x_perm, _C, m.x_perm, "x_perm"),
+                                                 _on(x_scale, _F, m.x_scale, "x_scale"),
+                                                 _on(offsets, _I, n.bounds, "offsets"), _on(w13, _C, m.w13, "w13"),
+                                                 _on(w13_scale, _F, m.w13_scale, "w13_scale"), _on(h, _C, m.h, "h"),
+                                                 _on(h_scale, _F, m.h_scale, "h_scale"), _on(ws, _U, 0, "ws"),
+                                                 _wsb(ws), _stream(stream))
+    if st:
+        raise MoEError(st, "moe_expert_up_fp8_block")
+
+
+def moe_expert_down_fp8_block(shape, h, h_scale, offsets, w2, w2_scale, y_perm, ws, stream=None):
+    """Down projection in block-scaled FP8 into y_perm (bfloat16)."""
+    n, m = _counts_of(bytes(shape)), _fp8_counts(bytes(shape))
+    st = (_lib or lib()).moe_expert_down_fp8_block(shape, _on(h, _C, m.h, "h"), _on(h_scale, _F, m.h_scale, "h_scale"),
+                                                   _on(offsets, _I, n.bounds, "offsets"), _on(w2, _C, m.w2, "w2"),
+                                                   _on(w2_scale, _F, m.w2_scale, "w2_scale"),
+                                                   _on(y_perm, _B, n.rows, "y_perm"), _on(ws, _U, 0, "ws"), _wsb(ws),
+                                                   _stream(stream))
+    if st:
+        raise MoEError(st, "moe_expert_down_fp8_block")
+
+
+def moe_layer_fp8_block(shape, logits, ids_in, w_in, x, w13, w13_scale, w2, w2_scale, out, ws, stream=None,
+                        residual=None):
+    """The layer with block-scaled FP8 experts (no shared experts)."""
+    n, m = _counts_of(bytes(shape)), _fp8_counts(bytes(shape))
+    st = (_lib or lib()).moe_layer_fp8_block(shape, _on(logits, _F, n.logits, "logits"),
+                                             _on(ids_in, _I, n.pairs, "ids_in"), _on(w_in, _F, n.pairs, "w_in"),
+                                             _on(x, _B, n.x, "x"), _on(w13, _C, m.w13, "w13"),
+                                             _on(w13_scale, _F, m.w13_scale, "w13_scale"), _on(w2, _C, m.w2, "w2"),
+                                             _on(w2_scale, _F, m.w2_scale, "w2_scale"),
+                                             _on(residual, _B, n.x, "residual"), _on(out, _B, n.x, "out"),
+                                             _on(ws, _U, 0, "ws"), _wsb(ws), _stream(stream))
+    if st:
+        raise MoEError(st, "moe_layer_fp8_block")
 
 
 def moe_ep_plan(experts: int, world: int, rank: int, capacity: int, counts_all):
