@@ -10,12 +10,20 @@
 // is one multiply-add (two at a time: fma.rn.f32x2).  TMEM holds 512 / (128 NSUB)
 // accumulators, so the MMAs of the next steps run while a step is added up.
 //
-// Roles: warp 0 loads by TMA, warp 1 issues the MMAs, warps 2..9 add up and store:
-// warp w owns TMEM lanes 32 (w % 4) .. +31 and columns 64 h .. 64 h + 63 (h = (w - 2) / 4)
-// of every block.  For SwiGLU the two blocks are the gate and up rows of the same 128
-// output columns, so a thread holds both factors of its 64 outputs; the activation is
-// quantized again as it is stored, and the two warps that share a row block exchange
-// their largest magnitude through shared memory.
+// Roles: warp 0 loads by TMA, warp 1 issues the MMAs, warps 4..11 add up and store:
+// warp w owns TMEM lanes 32 (w % 4) .. +31 and columns 64 h .. 64 h + 63 (h = (w - 4) / 4)
+// of every block.  Those eight take the registers that the first warpgroup gives up
+// (setmaxnreg): 128 sums and a piece of 64 columns.  For SwiGLU the two blocks are the
+// gate and up rows of the same 128 output columns, so a thread holds both factors of its
+// 64 outputs; the activation is quantized again as it is stored, and the two warps that
+// share a row block exchange their largest magnitude through shared memory.
+//
+// What bounds it at large sizes is the round trip of an accumulator: four MMAs (512
+// cycles) and 300 until the warps see them, then two reads of 64 columns (240 cycles
+// each, of which 175 are latency) with their multiply-adds and 250 around them.  Measured
+// and not kept: CTA pairs (M 256; half the shared-memory traffic, but the round trip
+// crosses SMs: 2 to 8 % slower), accumulators of one block each (up to 30 % slower), 16 or
+// 32 columns a read, scales brought by warps of their own.
 //
 // Persistent CTAs walk a tile list built from the bucket bounds, as in gemm.cu.  Every
 // wait is bounded (MOE_ERR_TIMEOUT); the exchange goes through an mbarrier so that it is,
@@ -27,9 +35,10 @@ namespace {
 
 constexpr int F_BM = 128;                       // activation rows per tile
 constexpr int F_BOX = 128 * 128;                // 128 rows of 128 codes
-constexpr int F_THREADS = 320;
+constexpr int F_THREADS = 384;
 constexpr int F_EPI_WARPS = 8;
-constexpr int F_MAX_SMEM = 216 * 1024;
+constexpr int F_MAX_SMEM = 227 * 1024;
+constexpr int F_STORE = 2048;                   // shared memory of a warp's output: 32 rows of 64 bytes
 constexpr int F_RASTER = 8;                     // column tiles of a band (tile order)
 
 template <int NSUB>
@@ -93,14 +102,33 @@ __device__ __forceinline__ unsigned long long fma_f32x2(unsigned long long a, un
     return r;
 }
 
-// tcgen05.wait::ld that the registers loaded before it pass through, so that no use of
-// them can be moved ahead of it.
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :: "memory");
+// 64 consecutive FP32 columns of this warp's 32 TMEM lanes as 32 pairs, waited for (load
+// and wait in one statement: no use of the registers can come before the wait).
+__device__ __forceinline__ void tmem_ld_pairs64(uint32_t taddr, unsigned long long (&r)[32]) {
+    asm volatile("{\n\t.reg .b32 t<64>;\n\ttcgen05.ld.sync.aligned.32x32b.x64.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31,t32,t33,t34,t35,t36,t37,t38,t39,t40,t41,t42,t43,t44,t45,t46,t47,t48,t49,t50,t51,t52,t53,t54,t55,t56,t57,t58,t59,t60,t61,t62,t63}, [%32];\n\ttcgen05.wait::ld.sync.aligned;\n\tmov.b64 %0, {t0,t1};\n\tmov.b64 %1, {t2,t3};\n\tmov.b64 %2, {t4,t5};\n\tmov.b64 %3, {t6,t7};\n\tmov.b64 %4, {t8,t9};\n\tmov.b64 %5, {t10,t11};\n\tmov.b64 %6, {t12,t13};\n\tmov.b64 %7, {t14,t15};\n\tmov.b64 %8, {t16,t17};\n\tmov.b64 %9, {t18,t19};\n\tmov.b64 %10, {t20,t21};\n\tmov.b64 %11, {t22,t23};\n\tmov.b64 %12, {t24,t25};\n\tmov.b64 %13, {t26,t27};\n\tmov.b64 %14, {t28,t29};\n\tmov.b64 %15, {t30,t31};\n\tmov.b64 %16, {t32,t33};\n\tmov.b64 %17, {t34,t35};\n\tmov.b64 %18, {t36,t37};\n\tmov.b64 %19, {t38,t39};\n\tmov.b64 %20, {t40,t41};\n\tmov.b64 %21, {t42,t43};\n\tmov.b64 %22, {t44,t45};\n\tmov.b64 %23, {t46,t47};\n\tmov.b64 %24, {t48,t49};\n\tmov.b64 %25, {t50,t51};\n\tmov.b64 %26, {t52,t53};\n\tmov.b64 %27, {t54,t55};\n\tmov.b64 %28, {t56,t57};\n\tmov.b64 %29, {t58,t59};\n\tmov.b64 %30, {t60,t61};\n\tmov.b64 %31, {t62,t63};\n\t}" : "=l"(r[0]),"=l"(r[1]),"=l"(r[2]),"=l"(r[3]),"=l"(r[4]),"=l"(r[5]),"=l"(r[6]),"=l"(r[7]),"=l"(r[8]),"=l"(r[9]),"=l"(r[10]),"=l"(r[11]),"=l"(r[12]),"=l"(r[13]),"=l"(r[14]),"=l"(r[15]),"=l"(r[16]),"=l"(r[17]),"=l"(r[18]),"=l"(r[19]),"=l"(r[20]),"=l"(r[21]),"=l"(r[22]),"=l"(r[23]),"=l"(r[24]),"=l"(r[25]),"=l"(r[26]),"=l"(r[27]),"=l"(r[28]),"=l"(r[29]),"=l"(r[30]),"=l"(r[31]) : "r"(taddr) : "memory");
 }
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Four steps' scales for a warp, copied while the four before are used: float [32 rows][4]
+// and float [2 blocks][4].
+struct FScales {
+    float a[32][4];
+    float w[2][4];
+};
+static_assert(2 * sizeof(FScales) <= F_STORE && sizeof(FScales) % 16 == 0, "two of them in a warp's output buffer");
 
 struct FTile { int g, nt, row0, rows; };        // first row of the tile and how many it holds
 
@@ -133,6 +161,36 @@ __device__ __forceinline__ FTile f_tile(int tile, const int* prefix, const int* 
     return t;
 }
 
+// A warp's piece of the output, 64 bytes (u) of each of its 32 rows, a row per lane: turned
+// around in shared memory so that four lanes write a row's 64 bytes (straight from the
+// registers a store instruction touches 32 rows: 7000 cycles for a 128 x 256 BF16 tile).
+// 16-byte piece c of row r lies at c ^ (r / 2 mod 4): no bank conflicts either way.
+// `out` + row * pitch + at: the first row's piece; `rows` of the 32 exist, and columns up to `end`.
+__device__ __forceinline__ void store_rows(uint8_t* stg, const uint32_t (&u)[16], int lane, uint8_t* out, long long row0,
+                                           int rows, long long pitch, int at, int end) {
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+    __syncwarp();
+    const int c = lane & 3;
+    if (at + 16 * c >= end) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        if (r < rows)
+            *reinterpret_cast<uint4*>(out + (row0 + r) * pitch + at + 16 * c) =
+                *reinterpret_cast<const uint4*>(stg + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    }
+}
+
+// Rows that the TMA loads of a CTA with `rows` rows of the tile bring: boxes of 8, 32 or
+// 128 rows.  The rows of the slot past them keep what they hold, which reaches only
+// output rows that are not stored.
+__device__ __forceinline__ int f_box(int rows) { return rows <= 8 ? 8 : rows <= 96 ? 32 : 128; }
+__device__ __forceinline__ int f_boxes(int rows) { return (rows + f_box(rows) - 1) / f_box(rows); }
+
 template <int MODE, int NSUB>
 __global__ void __launch_bounds__(F_THREADS, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
@@ -143,7 +201,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
-    FCtl* ctl = reinterpret_cast<FCtl*>(smem + C::STAGES * C::STAGE_BYTES);
+    uint8_t* store = smem + C::STAGES * C::STAGE_BYTES;              // [F_EPI_WARPS][F_STORE]
+    FCtl* ctl = reinterpret_cast<FCtl*>(store + F_EPI_WARPS * F_STORE);
     int* prefix = reinterpret_cast<int*>(ctl + 1);                    // [groups + 1]
     int* start = prefix + p.groups + 1;                               // [groups] first row, [groups] rows
     const uint32_t smem_base = smem_u32(smem);
@@ -206,79 +265,88 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const int total = ctl->total;
     volatile int* abort = &ctl->abort;
 
-    if (warp == 0) {
-        // ---------------- TMA producer ----------------
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            long long armed = 0;
-            for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-                const FTile t = f_tile<UP>(tile, prefix, start, p);
-                // rows the tile does not have are not loaded: whatever the slot holds there
-                // reaches only output rows that are not stored
-                const int box = t.rows <= 8 ? 8 : t.rows <= 96 ? 32 : 128;
-                const int boxes = (t.rows + box - 1) / box;
-                const int w0 = t.g * p.parts * p.N + t.nt * BN;
-                const int w1 = MODE == kGemmSwiGLU ? w0 + p.N : w0 + 128;
-                for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), ph ^ 1u, abort)) { ok = false; break; }
-                    const uint32_t full = smem_u32(&ctl->full[stage]);
-                    const uint32_t sa = smem_base + (uint32_t)(stage * C::STAGE_BYTES);
-                    mbar_arrive_expect_tx(full, (uint32_t)(NSUB * F_BOX + boxes * box * 128));
-                    tma_load_2d(sa + F_BOX, &tmW, full, kb * 128, w0);
-                    if (NSUB == 2) tma_load_2d(sa + 2 * F_BOX, &tmW, full, kb * 128, w1);
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");         // 128 x 40 + 256 x 232 = 384 x 168 registers
+        if (warp == 0) {
+            // ---------------- TMA producer (both CTAs of a pair) ----------------
+            if (lane == 0) {
+                int stage = 0;
+                uint32_t ph = 0;
+                bool ok = true;
+                long long armed = 0;
+                for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+                    const FTile t = f_tile<UP>(tile, prefix, start, p);
+                    const int box = f_box(t.rows), boxes = f_boxes(t.rows);
+                    const uint32_t bytes = (uint32_t)(NSUB * F_BOX + boxes * box * 128);
+                    const int w0 = t.g * p.parts * p.N + t.nt * BN;
+                    const int w1 = MODE == kGemmSwiGLU ? w0 + p.N : w0 + 128;
                     const CUtensorMap* m = box == 128 ? &tmA : box == 32 ? &tmA32 : &tmA8;
-                    for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(sa + (uint32_t)(i * box * 128), m, full, kb * 128, t.row0 + i * box);
-                    ++armed;
-                    if (++stage == C::STAGES) { stage = 0; ph ^= 1u; }
+                    for (int kb = 0; kb < p.nkb; ++kb) {
+                        if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), ph ^ 1u, abort)) { ok = false; break; }
+                        const uint32_t full = smem_u32(&ctl->full[stage]);
+                        const uint32_t sa = smem_base + (uint32_t)(stage * C::STAGE_BYTES);
+                        mbar_arrive_expect_tx(full, bytes);
+                        tma_load_2d(sa + F_BOX, &tmW, full, kb * 128, w0);
+                        if (NSUB == 2) tma_load_2d(sa + 2 * F_BOX, &tmW, full, kb * 128, w1);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(sa + (uint32_t)(i * box * 128), m, full, kb * 128, t.row0 + i * box);
+                        ++armed;
+                        if (++stage == C::STAGES) { stage = 0; ph ^= 1u; }
+                    }
+                }
+                if (!ok) {
+                    if (!wait_armed_stages(smem_u32(&ctl->full[0]), C::STAGES, armed)) settle_delay();
+                    raise_status(p.hdr, MOE_ERR_TIMEOUT);
+                    p.hdr->timeout_site = kSiteGemmProducer;
                 }
             }
-            if (!ok) {
-                if (!wait_armed_stages(smem_u32(&ctl->full[0]), C::STAGES, armed)) settle_delay();
-                raise_status(p.hdr, MOE_ERR_TIMEOUT);
-                p.hdr->timeout_site = kSiteGemmProducer;
-            }
-        }
-    } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
-        if (lane == 0) {
+        } else if (warp == 1) {
+            // ---------------- MMA issuer ----------------
+            // The whole warp walks the loop and one elected lane issues: descriptors and
+            // barriers stay in uniform registers (in a block of lane 0 alone an instruction
+            // took 65 cycles to issue, here about 30).
             constexpr uint32_t idesc = idesc_e4m3_f32(F_BM, C::ACC_COLS);
+            const bool leader = elect_one();
             int stage = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true;
             for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
                 for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (!mbar_wait_bounded(smem_u32(&ctl->full[stage]), ph, abort) ||
-                        !mbar_wait_bounded(smem_u32(&ctl->tempty[acc]), aph ^ 1u, abort)) { ok = false; break; }
+                    if (!mbar_wait_warp(smem_u32(&ctl->full[stage]), ph, abort)) { ok = false; break; }
+                    if (!mbar_wait_warp(smem_u32(&ctl->tempty[acc]), aph ^ 1u, abort)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t sa = smem_base + (uint32_t)(stage * C::STAGE_BYTES);
-                    const uint64_t ad = sdesc_k_sw128(sa), bd = sdesc_k_sw128(sa + F_BOX);
-                    const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
+                    if (leader) {
+                        const uint32_t sa = smem_base + (uint32_t)(stage * C::STAGE_BYTES);
+                        const uint64_t ad = sdesc_k_sw128(sa), bd = sdesc_k_sw128(sa + F_BOX);
+                        const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_e4m3(d, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc, kk > 0 ? 1u : 0u);
-                    tc_commit(smem_u32(&ctl->empty[stage]));
-                    tc_commit(smem_u32(&ctl->tfull[acc]));
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_e4m3(d, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc, kk > 0 ? 1u : 0u);
+                        tc_commit(smem_u32(&ctl->tfull[acc]));
+                        tc_commit(smem_u32(&ctl->empty[stage]));
+                    }
+                    __syncwarp();
                     if (++stage == C::STAGES) { stage = 0; ph ^= 1u; }
                     if (++acc == C::ACCS) { acc = 0; aph ^= 1u; }
                 }
             }
-            // every MMA this thread issued has completed before TMEM is freed
-            tc_commit(smem_u32(&ctl->drain));
+            // every MMA issued has completed before TMEM is freed
+            if (leader) tc_commit(smem_u32(&ctl->drain));
+            __syncwarp();
             volatile int never = 0;
-            const bool drained = mbar_wait_bounded(smem_u32(&ctl->drain), 0, &never);
-            if (!ok || !drained) {
+            const bool drained = mbar_wait_warp(smem_u32(&ctl->drain), 0, &never);
+            if (lane == 0 && (!ok || !drained)) {
                 raise_status(p.hdr, MOE_ERR_TIMEOUT);
                 p.hdr->timeout_site = kSiteGemmMma;
                 *abort = 1;
             }
         }
     } else {
-        // ---------------- adding up, activation, store (warps 2..9) ----------------
-        const int q = warp & 3, hf = (warp - 2) >> 2;
-        const int rl = 32 * q + lane;                                 // row of the tile
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        // ---------------- adding up, activation, store (warps 4..11) ----------------
+        const int q = warp & 3, hf = (warp - 4) >> 2;
+        const int rl = 32 * q + lane;                                 // row of this CTA's part of the tile
+        uint8_t* stg = store + (size_t)(warp - 4) * F_STORE;
         int acc = 0, parity = 0;
         uint32_t aph = 0;
         bool ok = true;
@@ -298,13 +366,29 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             for (int s = 0; s < NSUB; ++s)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sum[s][i] = 0ull;
-            float sa = __ldg(as), s0 = __ldg(ws0), s1 = NSUB == 2 ? __ldg(ws1) : 0.f;
+            // the scales come through the warp's piece of the output buffer, which is idle until
+            // the tile ends (a load to a register in this loop held its warp up by 15 %)
+            FScales* sc = reinterpret_cast<FScales*>(stg);            // [2]
+            auto fetch = [&](int k0) {
+                FScales* d = sc + ((k0 >> 2) & 1);
+                if (p.nkb % 4 == 0) {                                 // rows of scales are 16-byte aligned
+                    cp_async16(smem_u32(d->a[lane]), as + k0);
+                } else {
+                    for (int i = 0; i < 4; ++i) cp_async4(smem_u32(&d->a[lane][i]), as + min(k0 + i, p.nkb - 1));
+                }
+                if (lane < 4 * NSUB) cp_async4(smem_u32(&d->w[lane >> 2][lane & 3]), (lane < 4 ? ws0 : ws1) + min(k0 + (lane & 3), p.nkb - 1));
+            };
+            __syncwarp();                                             // the tile before has read its output there
+            fetch(0);
             for (int kb = 0; kb < p.nkb; ++kb) {
-                float f[2] = {sa * s0, sa * s1};
-                const int nx = kb + 1 < p.nkb ? kb + 1 : kb;          // the next step's scales
-                sa = __ldg(as + nx);
-                s0 = __ldg(ws0 + nx);
-                if (NSUB == 2) s1 = __ldg(ws1 + nx);
+                if ((kb & 3) == 0) {
+                    cp_async_wait();
+                    __syncwarp();
+                    if (kb + 4 < p.nkb) fetch(kb + 4);
+                }
+                const FScales* d = sc + ((kb >> 2) & 1);
+                const float sa = d->a[lane][kb & 3];
+                const float f[2] = {sa * d->w[0][kb & 3], NSUB == 2 ? sa * d->w[1][kb & 3] : 0.f};
                 if (!mbar_wait_warp(smem_u32(&ctl->tfull[acc]), aph, abort)) {
                     if (lane == 0) {
                         raise_status(p.hdr, MOE_ERR_TIMEOUT);
@@ -316,50 +400,36 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 tc_fence_after();
                 if (any) {
                     const uint32_t ta = tmem + (uint32_t)(acc * C::ACC_COLS + 64 * hf) + ((uint32_t)(32 * q) << 16);
-                    uint32_t v[2][16];
-                    tmem_ld_16cols(ta, v[0]);
 #pragma unroll
-                    for (int c = 0; c < 4 * NSUB; ++c) {              // 16-column pieces
-                        tmem_ld_wait16(v[c & 1]);
-                        if (c + 1 < 4 * NSUB)
-                            tmem_ld_16cols(ta + (uint32_t)(((c + 1) >> 2) * 128 + ((c + 1) & 3) * 16), v[(c + 1) & 1]);
-                        const unsigned long long ff = pack_f32x2(f[c >> 2], f[c >> 2]);
+                    for (int s = 0; s < NSUB; ++s) {
+                        unsigned long long v[32];
+                        tmem_ld_pairs64(ta + (uint32_t)(s * 128), v);
+                        const unsigned long long ff = pack_f32x2(f[s], f[s]);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const unsigned long long pv = pack_f32x2(__uint_as_float(v[c & 1][2 * i]),
-                                                                     __uint_as_float(v[c & 1][2 * i + 1]));
-                            sum[c >> 2][(c & 3) * 8 + i] = fma_f32x2(pv, ff, sum[c >> 2][(c & 3) * 8 + i]);
-                        }
+                        for (int i = 0; i < 32; ++i) sum[s][i] = fma_f32x2(v[i], ff, sum[s][i]);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[acc]));
+                { tc_fence_before(); __syncwarp(); if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[acc])); }
                 if (++acc == C::ACCS) { acc = 0; aph ^= 1u; }
             }
             if (!ok) break;
             const int col = t.nt * BN + 64 * hf;                      // first column of this thread's 64, block 0
             if (MODE == kGemmPlain) {
-                if (mine) {
-                    uint16_t* o = static_cast<uint16_t*>(p.out) + (size_t)row * p.N;
 #pragma unroll
-                    for (int s = 0; s < NSUB; ++s)
+                for (int s = 0; s < NSUB; ++s)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {                 // 8 columns at a time (N is a multiple of 16)
-                            const int c = col + 128 * s + 8 * i;
-                            if (c < p.N) {
-                                uint32_t u[4];
+                    for (int j = 0; j < 2; ++j) {                     // 32 columns at a time
+                        uint32_t u[16];
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    float a, b;
-                                    unpack_f32x2(sum[s][4 * i + j], a, b);
-                                    const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
-                                    u[j] = *reinterpret_cast<const uint32_t*>(&h2);
-                                }
-                                *reinterpret_cast<uint4*>(o + c) = make_uint4(u[0], u[1], u[2], u[3]);
-                            }
+                        for (int i = 0; i < 16; ++i) {
+                            float a, b;
+                            unpack_f32x2(sum[s][16 * j + i], a, b);
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+                            u[i] = *reinterpret_cast<const uint32_t*>(&h2);
                         }
-                }
+                        store_rows(stg, u, lane, static_cast<uint8_t*>(p.out), t.row0 + 32 * q, t.rows - 32 * q,
+                                   2 * (long long)p.N, 2 * (col + 128 * s + 32 * j), 2 * p.N);
+                    }
             } else {
                 constexpr int NB = MODE == kGemmSwiGLU ? 1 : NSUB;    // output blocks
                 // the activation, in place in the first NB blocks' registers
@@ -394,29 +464,21 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     ok = false;
                     break;
                 }
-                if (mine) {
-                    uint8_t* o = static_cast<uint8_t*>(p.out) + (size_t)row * p.N;
 #pragma unroll
-                    for (int s = 0; s < NB; ++s) {
-                        if (b0 + s >= p.nnb) break;
-                        const Fp8Quant qq = fp8_quant(amax_nan(ctl->amax[parity][s][0][rl], ctl->amax[parity][s][1][rl]));
-                        if (hf == 0) p.out_scale[(size_t)row * p.nnb + b0 + s] = qq.scale;
+                for (int s = 0; s < NB; ++s) {
+                    if (b0 + s >= p.nnb) break;
+                    const Fp8Quant qq = fp8_quant(amax_nan(ctl->amax[parity][s][0][rl], ctl->amax[parity][s][1][rl]));
+                    if (mine && hf == 0) p.out_scale[(size_t)row * p.nnb + b0 + s] = qq.scale;
+                    uint32_t u[16];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {                 // 16 columns at a time
-                            const int c = col + 128 * s + 16 * i;
-                            if (c < p.N) {
-                                uint32_t u[4];
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    float x[4];
-                                    unpack_f32x2(sum[s][8 * i + 2 * j], x[0], x[1]);
-                                    unpack_f32x2(sum[s][8 * i + 2 * j + 1], x[2], x[3]);
-                                    u[j] = fp8_quant4(qq, x[0], x[1], x[2], x[3]);
-                                }
-                                *reinterpret_cast<uint4*>(o + c) = make_uint4(u[0], u[1], u[2], u[3]);
-                            }
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        float x[4];
+                        unpack_f32x2(sum[s][2 * i], x[0], x[1]);
+                        unpack_f32x2(sum[s][2 * i + 1], x[2], x[3]);
+                        u[i] = fp8_quant4(qq, x[0], x[1], x[2], x[3]);
                     }
+                    store_rows(stg, u, lane, static_cast<uint8_t*>(p.out), t.row0 + 32 * q, t.rows - 32 * q,
+                               p.N, col + 128 * s, p.N);
                 }
             }
         }
@@ -433,19 +495,20 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
 template <int MODE, int NSUB>
 moe_status launch_f(const Fp8Problem& g, FParams p, const CUtensorMap& mw, const CUtensorMap (&ma)[3], cudaStream_t st) {
+    using C = FCfg<NSUB>;
     constexpr int BN = MODE == kGemmSwiGLU ? 128 : 128 * NSUB;
     p.ntn = (g.N + BN - 1) / BN;
-    const size_t smem = 1024 + (size_t)FCfg<NSUB>::STAGES * FCfg<NSUB>::STAGE_BYTES + sizeof(FCtl) +
-                        (size_t)(3 * g.groups + 1) * sizeof(int);
+    const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + F_EPI_WARPS * F_STORE +
+                        sizeof(FCtl) + (size_t)(3 * g.groups + 1) * sizeof(int);
     // the attribute belongs to the device that is current: set with every launch
     cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<MODE, NSUB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          F_MAX_SMEM);
     if (e == cudaSuccess) {
         const long long used = g.rows < g.groups ? g.rows : g.groups;
-        const long long tiles = (g.rows / F_BM + used) * p.ntn;       // at most
+        const long long tiles = (g.rows / F_BM + used) * p.ntn;     // at most
         const int sms = device_sm_count();
-        e = launch_kernel(fp8_gemm_kernel<MODE, NSUB>, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(F_THREADS),
-                          smem, st, 1, kUsePdl, ma[0], ma[1], ma[2], mw, p);
+        e = launch_kernel(fp8_gemm_kernel<MODE, NSUB>, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(F_THREADS), smem,
+                          st, 1, kUsePdl, ma[0], ma[1], ma[2], mw, p);
     }
     if (e == cudaSuccess) return MOE_OK;
     set_error("FP8 GEMM launch (smem %zu): %s", smem, cudaGetErrorString(e));

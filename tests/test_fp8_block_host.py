@@ -180,9 +180,13 @@ def test_the_binding_refuses_tensors_that_do_not_fit(L, act, call, arg):
 
 
 def test_waits_of_the_fp8_kernel():
-    """The rules of the other GEMMs: a warp gives up a wait as a whole, no unbounded barrier
-    between roles."""
-    W.test_a_warp_gives_up_a_wait_as_a_whole("gemm_fp8.cu")
-    for kernel, body in W.kernels("gemm_fp8.cu"):
-        assert "bar.sync" not in body
-        assert "__syncthreads" not in body[body.index("if (warp == 0) {"):body.rindex("tc_fence_before")]
+    """The rules of the other GEMMs: a warp gives up a wait as a whole (a wait that is not the
+    warp's stands in a block of one thread), and no barrier without a limit between roles."""
+    import re
+    (kernel, body), = W.kernels("gemm_fp8.cu")
+    alone = list(re.finditer(r"\b(mbar_wait_bounded|wait_armed_stages)\(", body))
+    assert len(alone) == 2 and body.count("mbar_wait_warp(") == 5
+    for m in alone:
+        assert any(W.SINGLE.search(h) for h in W.enclosing(body, m.start())), body[m.start():m.start() + 70]
+    roles = body[body.index("if (warp < 4) {"):body.rindex("tc_fence_before")]
+    assert "bar.sync" not in roles and "__syncthreads" not in roles

@@ -111,6 +111,7 @@ def test_dispatch_over_capacity_moves_nothing():
 # ---- products ------------------------------------------------------------------------
 BUCKETS = {
     "one": [1], "few": [0, 3, 0, 8, 9, 1], "edges": [32, 33, 96, 97, 127, 128, 129], "big": [300, 0, 513],
+    "mixed": [1, 8, 129, 200, 256, 257, 700, 1000],
     "many": [(7 * i) % 11 for i in range(300)],
 }
 WIDTHS = [(16, 16), (128, 128), (144, 112), (272, 400), (1024, 640), (2064, 144)]
@@ -172,11 +173,12 @@ def test_no_rows():
     assert torch.all(h == 9) and torch.all(hs == 7) and torch.all(y == 5)
 
 
+@pytest.mark.parametrize("rows", [400, 1200])
 @pytest.mark.parametrize("act", ["swiglu", "relu2"])
-def test_a_row_does_not_depend_on_its_company(act):
-    """A row alone and among 400 others: the same bits."""
+def test_a_row_does_not_depend_on_its_company(act, rows):
+    """A row alone and among 400 or 1200 others: the same bits."""
     H, I = 400, 272
-    d = problem([400, 17], H, I, act, seed=8, extra=0)
+    d = problem([rows, 17], H, I, act, seed=8, extra=0)
 
     def run(offsets, x, xs, R):
         shape = N.make_shape(R, H, 2, 1, I, act=ACT[act])
@@ -188,11 +190,11 @@ def test_a_row_does_not_depend_on_its_company(act):
         assert N.moe_status_read(ws) == N.MOE_OK
         return h, hs, y
 
-    whole = run(d["offsets"], d["x"], d["x_scale"], 417)
-    again = run(d["offsets"], d["x"], d["x_scale"], 417)
+    whole = run(d["offsets"], d["x"], d["x_scale"], rows + 17)
+    again = run(d["offsets"], d["x"], d["x_scale"], rows + 17)
     for a, b in zip(whole, again):
         assert torch.equal(a.view(U8), b.view(U8))
-    for r, bounds in ((0, [0, 1, 1]), (131, [0, 1, 1]), (399, [0, 1, 1]), (405, [0, 0, 1])):
+    for r, bounds in ((0, [0, 1, 1]), (131, [0, 1, 1]), (rows - 1, [0, 1, 1]), (rows + 5, [0, 0, 1])):
         alone = run(torch.tensor(bounds, dtype=I32, device=dev()), d["x"][r:r + 1].clone(), d["x_scale"][r:r + 1].clone(), 1)
         for a, b in zip(whole, alone):
             assert torch.equal(a[r:r + 1].view(U8), b.view(U8)), r
