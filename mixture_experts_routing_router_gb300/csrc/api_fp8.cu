@@ -56,6 +56,8 @@ moe_status do_dispatch(const moe_shape& s, const uint16_t* x, const int32_t* ids
                        int32_t* dest, int32_t* sorted_pair, uint8_t* x_perm, float* x_scale, void* ws, cudaStream_t st) {
     const WsLayout L = ws_layout(s);
     WsHeader* hdr = at<WsHeader>(ws, 0);
+    if (dispatch_fp8_small(s))
+        return from_cuda(launch_dispatch_fp8_small(s, x, ids, counts, offsets, dest, sorted_pair, x_perm, x_scale, hdr, st));
     int32_t* rank = at<int32_t>(ws, L.rank);
     const cudaError_t e = launch_count(s, ids, counts, offsets, rank, at<unsigned long long>(ws, L.flags),
                                        L.count_tiles, hdr, st);

@@ -2,8 +2,8 @@
 // on the way (fp8.cuh): x_perm[dest[p]] = codes of x[p / k], x_scale[dest[p]] their scales.
 //
 // Placement as in scatter_kernel (counts and ranks come from the same count kernel).  A
-// block takes a token; 16 lanes share a 128-column block of the row, 8 columns each, find
-// its largest magnitude with four shuffles and write the codes to the token's k slots.
+// block takes a token; 8 lanes share a 128-column block of the row, 16 columns each, find
+// its largest magnitude with three shuffles and write the codes to the token's k slots.
 // Bound by HBM: H * 2 bytes read and k * (H + H / 32) written a token.
 #include "fp8.cuh"
 
@@ -11,6 +11,41 @@ namespace moe {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
+
+// Four 128-column blocks, b0 .. b0 + 3, of a row (`src`, H columns) on one warp, 16 columns
+// a lane, to the slots dsh[0 .. k-1] (negative ones are left out).
+__device__ __forceinline__ void quantize_four_blocks(const uint16_t* src, int H, int nb, int b0, int lane, int k,
+                                                     const int* dsh, uint8_t* x_perm, float* x_scale) {
+    const int c = b0 * 128 + lane * 16;            // this lane's columns
+    const bool in = c < H;
+    uint32_t u[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    if (in) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src + c)), w = __ldcs(reinterpret_cast<const uint4*>(src + c) + 1);
+        u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+        u[4] = w.x; u[5] = w.y; u[6] = w.z; u[7] = w.w;
+    }
+    float f[16], m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        m = amax_nan(amax_nan(m, f[2 * i]), f[2 * i + 1]);
+    }
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) m = amax_nan(m, __shfl_xor_sync(kAll, m, off));
+    const Fp8Quant q = fp8_quant(m);
+    uint32_t code[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) code[i] = fp8_quant4(q, f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    const int b = b0 + (lane >> 3);
+    const bool lead = (lane & 7) == 0 && b < nb;
+    for (int j = 0; j < k; ++j) {
+        const int d = dsh[j];
+        if (d < 0) continue;
+        if (in) *reinterpret_cast<uint4*>(x_perm + (size_t)d * H + c) = make_uint4(code[0], code[1], code[2], code[3]);
+        if (lead) x_scale[(size_t)d * nb + b] = q.scale;
+    }
+}
 
 __global__ void __launch_bounds__(256)
 scatter_fp8_kernel(int T, int H, int k, int E, const uint16_t* __restrict__ x, const int32_t* __restrict__ ids,
@@ -22,8 +57,8 @@ scatter_fp8_kernel(int T, int H, int k, int E, const uint16_t* __restrict__ x, c
     if (hdr->cap_exceeded) return;                 // over capacity: no payload moves
     __shared__ int dsh[32];
     const long long R = (long long)T * k;
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, sub = lane & 15;
-    const int HV = H / 8, nb = (H + kFp8Block - 1) / kFp8Block;
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
+    const int nb = (H + kFp8Block - 1) / kFp8Block;
     const int warps = nt >> 5, warp = tid >> 5;
     for (int t = blockIdx.x; t < T; t += gridDim.x) {
         if (tid < k) {
@@ -40,45 +75,150 @@ scatter_fp8_kernel(int T, int H, int k, int E, const uint16_t* __restrict__ x, c
             dsh[tid] = d;
         }
         __syncthreads();
-        const uint4* src = reinterpret_cast<const uint4*>(x) + (size_t)t * HV;
-        // a warp takes two 128-column blocks at a time
-        for (int b0 = 2 * warp; b0 < nb; b0 += 2 * warps) {
-            const int c = b0 * 16 + lane;          // 8-column group of this lane
-            const bool in = c < HV;
-            const uint4 v = in ? __ldcs(src + c) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-            float f[8], m = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(u[i] << 16);
-                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-                m = amax_nan(amax_nan(m, f[2 * i]), f[2 * i + 1]);
-            }
-#pragma unroll
-            for (int off = 8; off > 0; off >>= 1) m = amax_nan(m, __shfl_xor_sync(kAll, m, off));
-            const Fp8Quant q = fp8_quant(m);
-            const uint2 code = make_uint2(fp8_quant4(q, f[0], f[1], f[2], f[3]), fp8_quant4(q, f[4], f[5], f[6], f[7]));
-            const int b = b0 + (lane >> 4);
-            for (int j = 0; j < k; ++j) {
-                const int d = dsh[j];
-                if (d < 0) continue;
-                if (in) *reinterpret_cast<uint2*>(x_perm + (size_t)d * H + 8 * c) = code;
-                if (sub == 0 && b < nb) x_scale[(size_t)d * nb + b] = q.scale;
-            }
-        }
+        for (int b0 = 4 * warp; b0 < nb; b0 += 4 * warps)
+            quantize_four_blocks(x + (size_t)t * H, H, nb, b0, lane, k, dsh, x_perm, x_scale);
         __syncthreads();
+    }
+}
+
+// The whole dispatch of up to kSmallPairs pairs in one launch: every block counts all pairs
+// (and those before its own tokens') in shared memory, so that none waits for another;
+// then it places and quantizes its tokens.  1024 tokens x 2048, k = 6, 64 experts: SMALL_MID
+// us, against 14.2 of clearing the look-back flags, counting and scattering in turn.
+// Stable, and what is valid, as count_kernel and scatter_kernel have it: the slot of pair p
+// is offsets[e] + the valid pairs of e before p.
+constexpr int kSmallThreads = 1024;
+
+__global__ void __launch_bounds__(kSmallThreads)
+dispatch_fp8_kernel(int T, int H, int k, int E, int capacity, const uint16_t* __restrict__ x,
+                    const int32_t* __restrict__ ids, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
+                    int32_t* __restrict__ dest, int32_t* __restrict__ sorted_pair, uint8_t* __restrict__ x_perm,
+                    float* __restrict__ x_scale, WsHeader* hdr) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ int sm[];
+    int* total = sm;                               // [E], then its exclusive scan
+    int* before = total + E;                       // [E] of the pairs before this block's
+    int* mine = before + E;                        // [own pairs] expert (-1: invalid), then slot
+    __shared__ int wsum[kSmallThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int t0 = (int)((long long)T * blockIdx.x / gridDim.x), t1 = (int)((long long)T * (blockIdx.x + 1) / gridDim.x);
+    const bool lead = blockIdx.x == 0;
+    for (int e = tid; e < 2 * E; e += kSmallThreads) sm[e] = 0;
+    __syncthreads();
+    // whole tokens a warp: lanes of a token sit together, the first of equal ids counts
+    const int tpw = 32 / k, used = tpw * k, step = (kSmallThreads / 32) * tpw, j = lane % k;
+    constexpr int kAhead = 8;                      // loads under way together
+    for (int tb = warp * tpw; tb < T; tb += kAhead * step) {
+        int next[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int t = tb + u * step + lane / k;
+            next[u] = lane < used && t < T ? __ldg(ids + (size_t)(tb + u * step) * k + lane) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (tb + u * step >= T) break;
+            const int t = tb + u * step + lane / k, id = next[u];
+            const bool pair = lane < used && t < T;
+            bool ok = pair && id >= 0 && id < E;
+            for (int b = 1; b < k; ++b) {          // (a match over the warp took 60 cycles of the SM)
+                const int earlier = __shfl_up_sync(kAll, id, b);
+                ok = ok && !(j >= b && earlier == id);
+            }
+            if (ok) {
+                atomicAdd(&total[id], 1);
+                if (t < t0) atomicAdd(&before[id], 1);
+            }
+            if (pair && !ok && lead) raise_status(hdr, MOE_ERR_INVALID_ROUTE);
+            if (pair && t >= t0 && t < t1) mine[(t - t0) * k + j] = ok ? id : -1;
+        }
+    }
+    __syncthreads();
+    // ---- exclusive scan of the counts; capacity
+    const int per = (E + kSmallThreads - 1) / kSmallThreads, e0 = tid * per;
+    int loc = 0, over = 0;
+    for (int e = e0; e < min(e0 + per, E); ++e) {
+        const int c = total[e];
+        if (lead) counts[e] = c;
+        over |= c > capacity;
+        loc += c;
+    }
+    int inc = loc;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(kAll, inc, off);
+        if (lane >= off) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    over = __syncthreads_or(over);
+    int run = inc - loc;
+    for (int w = 0; w < warp; ++w) run += wsum[w];
+    for (int e = e0; e < min(e0 + per, E); ++e) {
+        const int c = total[e];
+        total[e] = run;
+        if (lead) offsets[e] = run;
+        run += c;
+    }
+    if (lead && tid == kSmallThreads - 1) {
+        offsets[E] = run;
+        hdr->cap_exceeded = over;
+        if (over) raise_status(hdr, MOE_ERR_CAPACITY);
+    }
+    if (over) return;                              // over capacity: no payload moves
+    __syncthreads();
+    // ---- slots of this block's pairs
+    const int own = (t1 - t0) * k;                 // a thread each (dispatch_fp8_small)
+    int slot = -1;
+    if (tid < own) {
+        const int e = mine[tid];
+        if (e >= 0) {
+            slot = total[e] + before[e];
+            for (int j = 0; j < tid; ++j) slot += mine[j] == e;
+        }
+        dest[(size_t)t0 * k + tid] = slot;
+        if (slot >= 0) sorted_pair[slot] = t0 * k + tid;
+    }
+    __syncthreads();
+    if (tid < own) mine[tid] = slot;
+    __syncthreads();
+    // ---- rows
+    const int nb = (H + kFp8Block - 1) / kFp8Block, items = (nb + 3) / 4;
+    for (int i = warp; i < (t1 - t0) * items; i += kSmallThreads / 32) {
+        const int t = i / items, b0 = 4 * (i - t * items);
+        quantize_four_blocks(x + (size_t)(t0 + t) * H, H, nb, b0, lane, k, mine + t * k, x_perm, x_scale);
     }
 }
 
 }  // namespace
 
+// Up to this many pairs the counting of all of them by every block (ids from L2) costs less
+// than two more launches.
+constexpr long long kSmallPairs = 12288;
+
+bool dispatch_fp8_small(const moe_shape& s) {
+    const int sms = device_sm_count(), grid = s.tokens < sms ? s.tokens : sms;
+    return (long long)s.tokens * s.top_k <= kSmallPairs && (s.tokens + grid - 1) / grid * s.top_k <= kSmallThreads;
+}
+
+cudaError_t launch_dispatch_fp8_small(const moe_shape& s, const uint16_t* x, const int32_t* ids, int32_t* counts,
+                                      int32_t* offsets, int32_t* dest, int32_t* sorted_pair, uint8_t* x_perm,
+                                      float* x_scale, WsHeader* hdr, cudaStream_t st) {
+    const int sms = device_sm_count(), grid = s.tokens < sms ? s.tokens : sms;
+    const int own = (s.tokens + grid - 1) / grid * s.top_k;
+    const size_t smem = (size_t)(2 * s.experts + own) * sizeof(int);
+    return launch_kernel(dispatch_fp8_kernel, dim3((unsigned)grid), dim3(kSmallThreads), smem, st, 1, kUsePdl, s.tokens,
+                         s.hidden, s.top_k, s.experts, s.capacity, x, ids, counts, offsets, dest, sorted_pair, x_perm,
+                         x_scale, hdr);
+}
+
 cudaError_t launch_scatter_fp8(const moe_shape& s, const uint16_t* x, const int32_t* ids, const int32_t* offsets,
                                const int32_t* rank, int32_t* dest, int32_t* sorted_pair, uint8_t* x_perm,
                                float* x_scale, WsHeader* hdr, cudaStream_t st) {
-    int threads = 32;
-    while (threads < 256 && threads < s.hidden / 8) threads *= 2;
+    // four blocks of the row a warp and pass, no pass with idle warps; a block a token
+    const int items = (fp8_blocks(s.hidden) + 3) / 4, passes = (items + 7) / 8, threads = 32 * ((items + passes - 1) / passes);
     long long blocks = s.tokens;
-    const long long cap = (long long)device_sm_count() * (2048 / threads);
+    const long long cap = (long long)device_sm_count() * 1024;
     if (blocks > cap) blocks = cap;
     return launch_kernel(scatter_fp8_kernel, dim3((unsigned)blocks), dim3(threads), 0, st, 1, kUsePdl, s.tokens,
                          s.hidden, s.top_k, s.experts, x, ids, offsets, rank, dest, sorted_pair, x_perm, x_scale,

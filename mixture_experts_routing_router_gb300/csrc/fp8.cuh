@@ -68,7 +68,12 @@ struct Fp8Problem {
 };
 moe_status launch_fp8_gemm(const Fp8Problem& p, WsHeader* hdr, cudaStream_t st);
 
-// launch_scatter with the rows quantized on the way.
+// The dispatch with the rows quantized on the way: in one launch for a small batch, else
+// launch_count and launch_scatter_fp8.
+bool dispatch_fp8_small(const moe_shape& s);
+cudaError_t launch_dispatch_fp8_small(const moe_shape& s, const uint16_t* x, const int32_t* ids, int32_t* counts,
+                                      int32_t* offsets, int32_t* dest, int32_t* sorted_pair, uint8_t* x_perm,
+                                      float* x_scale, WsHeader* hdr, cudaStream_t st);
 cudaError_t launch_scatter_fp8(const moe_shape& s, const uint16_t* x, const int32_t* ids, const int32_t* offsets,
                                const int32_t* rank, int32_t* dest, int32_t* sorted_pair, uint8_t* x_perm,
                                float* x_scale, WsHeader* hdr, cudaStream_t st);

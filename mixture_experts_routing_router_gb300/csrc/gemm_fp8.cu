@@ -72,7 +72,7 @@ struct FCtl {
     int abort;
     int total;
     int wtot[F_THREADS / 32];
-    float amax[2][2][2][F_BM];                  // [tile parity][block][column half][row]
+    float amax[2][2][2][F_BM];                  // [exchange parity][block][column half][row]
 };
 
 __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -130,14 +130,24 @@ struct FScales {
 };
 static_assert(2 * sizeof(FScales) <= F_STORE && sizeof(FScales) % 16 == 0, "two of them in a warp's output buffer");
 
+// 1 / (1 + e^-x): two of the approximate units' operations, 2^-21 of the value for |x| < 8
+// (e^-x overflows to infinity where the result is 0 to FP32's normal range).
+__device__ __forceinline__ float sigmoid_approx(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
 struct FTile { int g, nt, row0, rows; };        // first row of the tile and how many it holds
 
 // The tile list: group g's row tiles times column tiles, in bands of F_RASTER column
 // tiles.  The up projection (long rows) walks a band's column tiles first, the down
 // projection its row tiles (as gemm.cu, for the same reuse in L2).
+// `lo`: a group at or before the tile's (that of the role's last tile: they ascend).
 template <bool COLS_FIRST>
-__device__ __forceinline__ FTile f_tile(int tile, const int* prefix, const int* start, const FParams& p) {
-    int lo = 0, hi = p.groups;
+__device__ __forceinline__ FTile f_tile(int tile, int& lo, const int* prefix, const int* start, const FParams& p) {
+    int hi = p.groups;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (prefix[mid] <= tile) lo = mid; else hi = mid;
@@ -274,8 +284,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 uint32_t ph = 0;
                 bool ok = true;
                 long long armed = 0;
+                int group = 0;
                 for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-                    const FTile t = f_tile<UP>(tile, prefix, start, p);
+                    const FTile t = f_tile<UP>(tile, group, prefix, start, p);
                     const int box = f_box(t.rows), boxes = f_boxes(t.rows);
                     const uint32_t bytes = (uint32_t)(NSUB * F_BOX + boxes * box * 128);
                     const int w0 = t.g * p.parts * p.N + t.nt * BN;
@@ -350,36 +361,61 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int acc = 0, parity = 0;
         uint32_t aph = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, parity ^= 1) {
-            const FTile t = f_tile<UP>(tile, prefix, start, p);
-            const bool mine = rl < t.rows, any = 32 * q < t.rows;     // this row; a row of the warp
-            const int row = t.row0 + (mine ? rl : 0);
-            const float* as = p.a_scale + (size_t)row * p.nkb;
+        // The scales come through the warp's piece of the output buffer, which is idle until
+        // the tile ends (a load to a register in the K loop held its warp up by 15 %): four
+        // steps by cp.async while the four before are used.  A tile's first four are loaded to
+        // registers ahead of the output of the tile before.
+        FScales* sc = reinterpret_cast<FScales*>(stg);                // [2]
+        const float *as = nullptr, *ws = nullptr;                     // of this row; of lane / 4's block of weight rows
+        float a4[4] = {0.f, 0.f, 0.f, 0.f}, w1 = 0.f;
+        // The next 32 tiles of this CTA, one a lane (found once in 32 tiles: a search takes
+        // 1000 cycles, as much as a step of K).
+        FTile mytile = {0, 0, 0, 0}, t = {0, 0, 0, 0};
+        int seen = 0;
+        auto open_tile = [&](int tile) {
+            if ((seen & 31) == 0) {
+                int group = 0;
+                const long long mine_at = tile + (long long)lane * gridDim.x;
+                if (mine_at < total) mytile = f_tile<UP>((int)mine_at, group, prefix, start, p);
+                __syncwarp();
+            }
+            t.g = __shfl_sync(0xffffffffu, mytile.g, seen & 31);
+            t.nt = __shfl_sync(0xffffffffu, mytile.nt, seen & 31);
+            t.row0 = __shfl_sync(0xffffffffu, mytile.row0, seen & 31);
+            t.rows = __shfl_sync(0xffffffffu, mytile.rows, seen & 31);
+            ++seen;
+            as = p.a_scale + (size_t)(t.row0 + (rl < t.rows ? rl : 0)) * p.nkb;
+            // block rows of the weights' scales: the first block's, and the second's (SwiGLU: the up rows')
             const int b0 = t.nt * (BN / 128);
-            // the tile's weight scales: block rows b0 of the first block, and of the second
-            const size_t wrow = (size_t)t.g * p.parts * p.nnb + b0;
-            const float* ws0 = p.w_scale + wrow * p.nkb;
-            const float* ws1 = MODE == kGemmSwiGLU ? p.w_scale + (wrow + p.nnb) * p.nkb
-                                                   : ws0 + (b0 + 1 < p.nnb ? p.nkb : 0);
+            const int second = MODE == kGemmSwiGLU ? p.nnb : b0 + 1 < p.nnb ? 1 : 0;
+            ws = p.w_scale + ((size_t)t.g * p.parts * p.nnb + b0 + (lane < 4 ? 0 : second)) * p.nkb;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a4[i] = __ldg(as + min(i, p.nkb - 1));
+            if (lane < 4 * NSUB) w1 = __ldg(ws + min(lane & 3, p.nkb - 1));
+        };
+        auto fetch = [&](int k0) {
+            FScales* d = sc + ((k0 >> 2) & 1);
+            if (p.nkb % 4 == 0) {                                     // rows of scales are 16-byte aligned
+                cp_async16(smem_u32(d->a[lane]), as + k0);
+            } else {
+                for (int i = 0; i < 4; ++i) cp_async4(smem_u32(&d->a[lane][i]), as + min(k0 + i, p.nkb - 1));
+            }
+            if (lane < 4 * NSUB) cp_async4(smem_u32(&d->w[lane >> 2][lane & 3]), ws + min(k0 + (lane & 3), p.nkb - 1));
+        };
+        int tile = blockIdx.x;
+        if (tile < total) open_tile(tile);
+        while (tile < total && ok) {
+            const bool mine = rl < t.rows, any = 32 * q < t.rows;     // this row; a row of the warp
+            const int row = t.row0 + (mine ? rl : 0), b0 = t.nt * (BN / 128), col = t.nt * BN + 64 * hf;
+            const int row_w = t.row0 + 32 * q, rows_w = t.rows - 32 * q;      // the warp's first row, and how many exist
+            __syncwarp();                                             // the tile before has read its output there
+            *reinterpret_cast<float4*>(sc->a[lane]) = make_float4(a4[0], a4[1], a4[2], a4[3]);
+            if (lane < 4 * NSUB) sc->w[lane >> 2][lane & 3] = w1;
             unsigned long long sum[NSUB][32];
 #pragma unroll
             for (int s = 0; s < NSUB; ++s)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sum[s][i] = 0ull;
-            // the scales come through the warp's piece of the output buffer, which is idle until
-            // the tile ends (a load to a register in this loop held its warp up by 15 %)
-            FScales* sc = reinterpret_cast<FScales*>(stg);            // [2]
-            auto fetch = [&](int k0) {
-                FScales* d = sc + ((k0 >> 2) & 1);
-                if (p.nkb % 4 == 0) {                                 // rows of scales are 16-byte aligned
-                    cp_async16(smem_u32(d->a[lane]), as + k0);
-                } else {
-                    for (int i = 0; i < 4; ++i) cp_async4(smem_u32(&d->a[lane][i]), as + min(k0 + i, p.nkb - 1));
-                }
-                if (lane < 4 * NSUB) cp_async4(smem_u32(&d->w[lane >> 2][lane & 3]), (lane < 4 ? ws0 : ws1) + min(k0 + (lane & 3), p.nkb - 1));
-            };
-            __syncwarp();                                             // the tile before has read its output there
-            fetch(0);
             for (int kb = 0; kb < p.nkb; ++kb) {
                 if ((kb & 3) == 0) {
                     cp_async_wait();
@@ -409,11 +445,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         for (int i = 0; i < 32; ++i) sum[s][i] = fma_f32x2(v[i], ff, sum[s][i]);
                     }
                 }
-                { tc_fence_before(); __syncwarp(); if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[acc])); }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[acc]));
                 if (++acc == C::ACCS) { acc = 0; aph ^= 1u; }
             }
             if (!ok) break;
-            const int col = t.nt * BN + 64 * hf;                      // first column of this thread's 64, block 0
+            tile += gridDim.x;
+            if (tile < total) open_tile(tile);
+            if (!any) continue;                                       // as the other warp of these rows
             if (MODE == kGemmPlain) {
 #pragma unroll
                 for (int s = 0; s < NSUB; ++s)
@@ -427,7 +467,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
                             u[i] = *reinterpret_cast<const uint32_t*>(&h2);
                         }
-                        store_rows(stg, u, lane, static_cast<uint8_t*>(p.out), t.row0 + 32 * q, t.rows - 32 * q,
+                        store_rows(stg, u, lane, static_cast<uint8_t*>(p.out), row_w, rows_w,
                                    2 * (long long)p.N, 2 * (col + 128 * s + 32 * j), 2 * p.N);
                     }
             } else {
@@ -443,8 +483,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         if (MODE == kGemmSwiGLU) {
                             float ua, ub;
                             unpack_f32x2(sum[NSUB - 1][i], ua, ub);
-                            a = __fdividef(a, 1.0f + __expf(-a)) * ua;
-                            b = __fdividef(b, 1.0f + __expf(-b)) * ub;
+                            a = a * sigmoid_approx(a) * ua;
+                            b = b * sigmoid_approx(b) * ub;
                         } else {
                             a = a > 0.f || a != a ? a * a : 0.f;
                             b = b > 0.f || b != b ? b * b : 0.f;
@@ -477,9 +517,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         unpack_f32x2(sum[s][2 * i + 1], x[2], x[3]);
                         u[i] = fp8_quant4(qq, x[0], x[1], x[2], x[3]);
                     }
-                    store_rows(stg, u, lane, static_cast<uint8_t*>(p.out), t.row0 + 32 * q, t.rows - 32 * q,
+                    store_rows(stg, u, lane, static_cast<uint8_t*>(p.out), row_w, rows_w,
                                p.N, col + 128 * s, p.N);
                 }
+                parity ^= 1;
             }
         }
     }

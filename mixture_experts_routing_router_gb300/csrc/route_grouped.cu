@@ -12,13 +12,16 @@
 //   w_j   = scale * s_j, divided by the sum over the selection when `renorm`.
 //
 // Keys are defined through double so that every implementation selects the same
-// experts, but the double unit is slow here (two results a cycle and SM).  The kernel
+// experts, but the double unit is slow here (two results a cycle and SM; a token's scores
+// in double take a warp 10 us, in pairs of floats, route_df.cuh, about one).  The kernel
 // therefore works on FP32 keys with a bound on their error (`eps`, below) and checks
 // that every comparison the result hangs on -- chosen against other groups, each
 // selected key against the next one -- is decided by more than that; a token where one
 // is not (about one in a thousand with random logits) is selected again from the
-// defined keys.  Two experts of equal logit and bias have equal keys either way.
+// defined keys: the winners next to one another among themselves, all experts where the
+// groups are in doubt.  Two experts of equal logit and bias have equal keys either way.
 #include "common.cuh"
+#include "route_df.cuh"
 #include "route_warp.cuh"
 
 #include <climits>
@@ -44,18 +47,106 @@ __device__ __forceinline__ double warp_sum(double v) {
 }
 __device__ __forceinline__ float warp_max(float v) { return route_unkey(__reduce_max_sync(kAll, route_key(v))); }
 
-// The FP32 scores' error: |s~ - s| <= s 2^-18 + 2^-24 for the softmax (exponents of up to
-// 127 rounded to FP32 before the exponential, two units of its last place, a sum of up to
-// 1024 terms, one division) and <= 2^-21 for the sigmoid, whose slope s (1 - s) damps the
-// error of large exponents; one more FP32 rounding with the bias.  Two keys of magnitude
-// `mag` at most, further apart than this, are in their defined order.
-__device__ __forceinline__ float key_margin(bool softmax, float top_score, float mag) {
-    return (softmax ? 0x1p-23f + 0x1p-17f * top_score : 0x1p-20f) + 0x1p-22f * mag;
+// How far two FP32 keys have to be apart to be in their defined order: twice the scores'
+// error, and the rounding of keys of magnitude `mag` at most with the bias.
+//   sigmoid: 2^-21; its slope s (1 - s) damps the error of large exponents.
+//   softmax: of s = e^-d / Z with d = max - l, d rounded and the exponential (2 + d units
+//   of 2^-24, and d e^-d <= 0.37), the division (2) and Z's own error: its terms', whose
+//   weighted mean distance is at most ln(E / Z), and a sum of up to EPL + 5 additions.
+__device__ __forceinline__ float key_margin(float score_margin, float mag) { return score_margin + 0x1p-22f * mag; }
+
+// One defined key, of logit x with bias b (softmax: maximum `top`, normaliser z): in pairs
+// of floats, with `doubt` set where their rounding is; and in double.
+__device__ __forceinline__ float pair_key(float x, float b, bool softmax, float top, Df z, bool& doubt) {
+    if (!isfinite(x) || !isfinite(b)) return -INFINITY;
+    Df s;
+    if (softmax) {
+        s = df_div(df_exp(df_two_sum(x, -top)), z);
+    } else {
+        const Df one = {1.f, 0.f}, e = df_exp({-fabsf(x), 0.f});
+        s = df_div(x >= 0.f ? one : e, df_add(one, e));
+    }
+    doubt = doubt || df_near_middle(s);
+    return s.h + b;
+}
+__device__ __noinline__ float double_key(float x, float b, bool softmax, float top, double z) {
+    if (!isfinite(x) || !isfinite(b)) return -INFINITY;
+    return (float)(softmax ? exp((double)x - (double)top) / z : 1.0 / (1.0 + exp(-(double)x))) + b;
+}
+// (Functions of their own: few tokens come here, and their registers would be everyone's.)
+__device__ __noinline__ Df pair_normaliser(const float* __restrict__ row, int E, float top, int lane) {
+    Df z = {0.f, 0.f};
+#pragma unroll 2
+    for (int e = lane; e < E; e += 32) {
+        const float x = row[e];
+        if (isfinite(x)) z = df_add(z, df_exp(df_two_sum(x, -top)));
+    }
+    for (int off = 16; off > 0; off >>= 1) {
+        const Df o = {__shfl_xor_sync(kAll, z.h, off), __shfl_xor_sync(kAll, z.l, off)};
+        z = df_add(z, o);
+    }
+    return z;
+}
+__device__ __noinline__ double double_normaliser(const float* __restrict__ row, int E, float top, int lane) {
+    double z = 0.0;
+    for (int e = lane; e < E; e += 32) {
+        const float x = row[e];
+        z += isfinite(x) ? exp((double)x - (double)top) : 0.0;
+    }
+    return warp_sum(z);
+}
+// The whole row's keys.
+__device__ __noinline__ void exact_keys(const float* __restrict__ row, const float* __restrict__ bias, int E,
+                                        bool softmax, float top, float* out, int lane) {
+    const Df z = softmax ? pair_normaliser(row, E, top, lane) : Df{1.f, 0.f};
+    bool doubt = false;
+#pragma unroll 2
+    for (int e = lane; e < E; e += 32) out[e] = pair_key(row[e], bias ? bias[e] : 0.f, softmax, top, z, doubt);
+    if (!__any_sync(kAll, doubt)) return;
+    const double zd = softmax ? double_normaliser(row, E, top, lane) : 1.0;
+    for (int e = lane; e < E; e += 32) out[e] = double_key(row[e], bias ? bias[e] : 0.f, softmax, top, zd);
+}
+// Lanes 0 .. n-1 hold the experts `e` of a row that may come before or after one another:
+// lane r receives the one of rank r by its defined key.
+__device__ __noinline__ int exact_order(const float* __restrict__ row, const float* __restrict__ bias, int E, bool softmax,
+                                        float top, int e, int n, int lane) {
+    const Df z = softmax ? pair_normaliser(row, E, top, lane) : Df{1.f, 0.f};
+    bool doubt = false;
+    const float x = row[e], b = bias ? bias[e] : 0.f;
+    float key = lane < n ? pair_key(x, b, softmax, top, z, doubt) : 0.f;
+    if (__any_sync(kAll, doubt)) {
+        const double zd = softmax ? double_normaliser(row, E, top, lane) : 1.0;
+        if (lane < n) key = double_key(x, b, softmax, top, zd);
+    }
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        const float ki = __shfl_sync(kAll, key, i);
+        const int ei = __shfl_sync(kAll, e, i);
+        rank += ki > key || (ki == key && ei < e);
+    }
+    int out = e;
+    for (int i = 0; i < n; ++i) {
+        const int ri = __shfl_sync(kAll, rank, i), ei = __shfl_sync(kAll, e, i);
+        if (ri == lane) out = ei;
+    }
+    return out;
 }
 
-// EPL = experts per lane (E <= 32 * EPL); lane l holds experts l, l + 32, ...
-template <int EPL>
-__global__ void __launch_bounds__(256)
+__device__ __forceinline__ float fast_sigmoid(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
+// EPL = experts per lane (E <= 32 * EPL; FULL: equal); lane l holds experts l, l + 32, ...
+// Bound by instructions (16384 tokens of 256 experts, 8 groups: NOW_LARGE us; selects
+// instead of branches, and what a warp's tokens share kept in registers -- biases, a
+// key's place in shared memory and its group -- took it from 1500 to about 700 a token).
+// A lane keeps its two best candidates, so that most rounds of warp-wide argmax need no
+// pass over its keys; the comparisons are checked once, side by side, after the rounds.
+template <int EPL, bool FULL>
+__global__ void __launch_bounds__(256, EPL <= 8 ? 3 : 1)
 route_grouped_kernel(int T, int E, int k, const moe_router r, const float* __restrict__ logits,
                      const float* __restrict__ bias, int32_t* __restrict__ ids, float* __restrict__ w, WsHeader* hdr) {
     extern __shared__ float sm[];
@@ -69,92 +160,88 @@ route_grouped_kernel(int T, int E, int k, const moe_router r, const float* __res
     // `per` lanes share a group (G rounded up to a power of two, 32 / that each); a key lies
     // in shared memory at e + per * group, which keeps those lanes on banks of their own
     const int lg = 32 - __clz(G - 1), per = G > 1 ? 32 >> lg : 32;
-    const float inv_n = 1.0f / (float)n;
     float* row_keys = sm + (size_t)warp * (E + G * per);
+    const float inv_n = 1.0f / (float)n;
+    auto in = [&](int i) { return FULL || lane + 32 * i < E; };
+    float b[EPL];                                  // biases
+    int first[EPL];                                // per * group: the group's first lane, and its padding
+    bool bad_bias = false;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = lane + 32 * i;
+        b[i] = bias && in(i) ? __ldg(bias + e) : 0.f;
+        bad_bias = bad_bias || !isfinite(b[i]);
+        first[i] = in(i) ? per * (int)(((float)e + 0.5f) * inv_n) : 0;
+    }
+    bad_bias = __any_sync(kAll, bad_bias);
     for (int t = gwarp; t < T; t += nwarps) {
         const float* row = logits + (size_t)t * E;
-        float x[EPL], b[EPL];
-        bool bad = false;
-        float top = -INFINITY;
+        float x[EPL], probe = 0.f, top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = lane + 32 * i;
-            x[i] = -INFINITY;
-            b[i] = 0.f;
-            if (e < E) {
-                x[i] = __ldg(row + e);
-                if (bias) b[i] = __ldg(bias + e);
-                if (!isfinite(x[i]) || !isfinite(b[i])) {
-                    bad = true;
-                    x[i] = -INFINITY;
-                }
-            }
-            top = fmaxf(top, x[i]);
+        for (int i = 0; i < EPL; ++i) x[i] = in(i) ? __ldg(row + lane + 32 * i) : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) probe = fmaf(in(i) ? x[i] : 0.f, 0.f, probe);   // NaN if one is not finite
+        if (__any_sync(kAll, probe != 0.f) || bad_bias) {
+            if (lane == 0) raise_status(hdr, MOE_ERR_NONFINITE);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) x[i] = isfinite(x[i]) && isfinite(b[i]) ? x[i] : -INFINITY;
         }
-        if (__any_sync(kAll, bad) && lane == 0) raise_status(hdr, MOE_ERR_NONFINITE);
+        float z = 1.f;
         if (softmax) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) top = fmaxf(top, x[i]);
             top = warp_max(top);
             if (top == -INFINITY) top = 0.f;
         }
-        float z = 1.f;
         int sel_e = 0;
-        float sel_x = 0.f;
         for (int exact = 0; exact < 2; ++exact) {
-            // ---- keys: an unused slot 0, a non-finite logit that of -inf
-            uint32_t key[EPL];
-            float top_s = 0.f;
-            if (exact) {
-                double zd = 1.0;
-                if (softmax) {
-                    double sum = 0.0;
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i) sum += x[i] == -INFINITY ? 0.0 : exp((double)x[i] - (double)top);
-                    zd = warp_sum(sum);
-                }
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) {
-                    const double s = softmax ? exp((double)x[i] - (double)top) / zd : 1.0 / (1.0 + exp(-(double)x[i]));
-                    const float kv = x[i] == -INFINITY ? -INFINITY : (float)s + b[i];
-                    key[i] = lane + 32 * i < E ? route_key(kv) : 0u;
-                }
-            } else {
-                float s[EPL];
+            // ---- keys: -inf for a lane's unused places and for a logit that is not finite
+            float key[EPL], margin = 0x1p-20f;                       // the scores' part of key_margin
+            if (!exact) {
                 if (softmax) {
                     float sum = 0.f;
 #pragma unroll
                     for (int i = 0; i < EPL; ++i) {
-                        s[i] = __expf(x[i] - top);
-                        sum += s[i];
+                        key[i] = expf(x[i] - top);
+                        sum += key[i];
                     }
                     z = warp_sum(sum);
                     z = z > 0.f ? z : 1.f;
-                    top_s = 1.0f / z;
+                    const float top_s = 1.0f / z;
+                    margin = 0x1p-23f * top_s * (7.0f + fmaxf(__logf((float)E * top_s), 0.f) + (float)(EPL + 5));
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) key[i] *= top_s;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) key[i] = fast_sigmoid(x[i]);
                 }
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) {
-                    s[i] = softmax ? s[i] * top_s : __fdividef(1.0f, 1.0f + __expf(-x[i]));
-                    const float kv = x[i] == -INFINITY ? -INFINITY : s[i] + b[i];
-                    key[i] = lane + 32 * i < E ? route_key(kv) : 0u;
-                }
+                for (int i = 0; i < EPL; ++i) key[i] = x[i] == -INFINITY ? -INFINITY : key[i] + b[i];
+            } else {
+                __syncwarp();
+                exact_keys(row, bias, E, softmax, top, row_keys, lane);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) key[i] = in(i) ? row_keys[lane + 32 * i] : -INFINITY;
             }
-            bool sure = true;
             // ---- groups
             if (G > 1) {
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) {
-                    const int e = lane + 32 * i;
-                    if (e < E) row_keys[e + per * (int)(((float)e + 0.5f) * inv_n)] = route_unkey(key[i]);
-                }
+                for (int i = 0; i < EPL; ++i)
+                    if (in(i)) row_keys[lane + 32 * i + first[i]] = key[i];
                 __syncwarp();
-                const int g = lane / per;
+                const int g = lane >> (5 - lg);
                 float k1 = -INFINITY, k2 = -INFINITY;
-                if (g < G)
-                    for (int j = lane % per; j < n; j += per) {
-                        const float v = row_keys[g * (n + per) + j];
+                if (g < G) {
+                    const float* gk = row_keys + g * (n + per);
+#pragma unroll 4
+                    for (int j = lane & (per - 1); j < n; j += per) {
+                        const float v = gk[j];
                         k2 = fmaxf(k2, fminf(k1, v));
                         k1 = fmaxf(k1, v);
                     }
+                }
                 for (int off = per >> 1; off > 0; off >>= 1) {
                     const float o1 = __shfl_xor_sync(kAll, k1, off), o2 = __shfl_xor_sync(kAll, k2, off);
                     k2 = fmaxf(fminf(k1, o1), fmaxf(k2, o2));
@@ -163,64 +250,91 @@ route_grouped_kernel(int T, int E, int k, const moe_router r, const float* __res
                 const bool two = r.group_top == 2 && n > 1;
                 const float value = two ? k1 + k2 : k1;
                 int rank = 0;
+#pragma unroll 4
                 for (int q = 0; q < G; ++q) {
                     const float o = __shfl_sync(kAll, value, q * per);
-                    rank += o > value || (o == value && q < g);
+                    rank += (o > value) | ((o == value) & (q < g));
                 }
                 const bool held = g < G && rank < r.topk_groups;
                 const unsigned mask = __ballot_sync(kAll, held);
-                const uint32_t vk = route_key(value);
-                const uint32_t lo = __reduce_min_sync(kAll, held ? vk : 0xffffffffu);
-                const uint32_t hi = __reduce_max_sync(kAll, !held && g < G ? vk : 0u);
-                if (hi != 0u) {
-                    // two keys a side, and the rounding of their sum
+                if (!exact && r.topk_groups < G) {
+                    // the chosen groups against the others: two keys a side, and their sum's rounding
+                    const uint32_t vk = route_key(value);
+                    const float lo = route_unkey(__reduce_min_sync(kAll, held ? vk : 0xffffffffu));
+                    const float hi = route_unkey(__reduce_max_sync(kAll, !held && g < G ? vk : 0u));
                     const float mag = warp_max(g < G ? fabsf(k1) + (two ? fabsf(k2) : 0.f) : 0.f);
-                    sure = route_unkey(lo) - route_unkey(hi) > 2.0f * key_margin(softmax, top_s, mag);
+                    if (!(lo - hi > 2.0f * key_margin(margin, mag))) continue;       // again, from the defined keys
                 }
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) key[i] = (mask >> first[i]) & 1u ? key[i] : -INFINITY;
+            }
+            // ---- rounds of argmax.  A lane holds its two best keys (of equal ones the lower
+            // index first), as ordered bits; `gone`: those taken.  Lane j keeps the j-th winner.
+            uint32_t u1, u2;
+            int i1, i2;
+            unsigned gone = 0u;
+            auto two_best = [&]() {
+                float b1 = -INFINITY, b2 = -INFINITY;
+                i1 = i2 = 0;
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
-                    const int e = lane + 32 * i;
-                    if (e < E && !((mask >> (per * (int)(((float)e + 0.5f) * inv_n))) & 1u)) key[i] = 0u;
+                    const float v = (gone >> i) & 1u ? -INFINITY : key[i];
+                    const bool first_ = v > b1, second = v > b2;
+                    i2 = first_ ? i1 : second ? i : i2;
+                    i1 = first_ ? i : i1;
+                    b2 = fmaxf(b2, fminf(b1, v));
+                    b1 = fmaxf(b1, v);
                 }
-            }
-            // ---- k rounds of argmax; one more to see that the last one was clear
-            uint32_t best = 0u;
-            int bi = 0;
-            auto local_best = [&]() {
-                best = 0u;
-#pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (key[i] > best) { best = key[i]; bi = i; }
+                u1 = route_key(b1);
+                u2 = route_key(b2);
             };
-            local_best();
-            float prev = 0.f, prev_x = 0.f;
-            int prev_e = 0;
-            for (int j = 0; j < k + (exact ? 0 : 1); ++j) {
-                const uint32_t m = __reduce_max_sync(kAll, best);
-                if (m == 0u) break;                                  // every candidate is selected
-                const unsigned e = __reduce_min_sync(kAll, best == m ? (unsigned)(lane + 32 * bi) : 0xffffffffu);
-                const bool mine = (e & 31u) == (unsigned)lane;
-                float xv = 0.f;
-                if (mine) {
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i)
-                        if (i == (int)(e >> 5)) { xv = x[i]; key[i] = 0u; }
-                    local_best();
-                }
-                xv = __shfl_sync(kAll, xv, (int)(e & 31u));
-                const float kv = route_unkey(m);
-                if (!exact && j > 0 && !(prev - kv > key_margin(softmax, top_s, fmaxf(fabsf(prev), fabsf(kv))))) {
-                    const bool same = xv == prev_x && (!bias || __ldg(bias + e) == __ldg(bias + prev_e));
-                    sure = sure && same;
-                }
-                prev = kv;
-                prev_x = xv;
-                prev_e = (int)e;
-                if (lane == j && j < k) { sel_e = (int)e; sel_x = xv; }
+            two_best();
+            bool fresh = true;                                        // u2 is the second best
+            uint32_t my_key = 0u;
+            // The next winner, kept by lane j.  (With nothing left it is some expert's -inf: only
+            // after a logit or bias that is not finite.)
+            auto round = [&](int j) {
+                const uint32_t m = __reduce_max_sync(kAll, u1);
+                const int e = (int)__reduce_min_sync(kAll, u1 == m ? (unsigned)(lane + 32 * i1) : 0xffffffffu);
+                const bool won = (e & 31) == lane;
+                const bool refill = won && !fresh;
+                gone |= won ? 1u << i1 : 0u;
+                u1 = won ? u2 : u1;
+                i1 = won ? i2 : i1;
+                fresh = won ? !fresh : fresh;
+                if (refill) two_best();
+                sel_e = lane == j ? (FULL ? e : min(e, E - 1)) : sel_e;
+                my_key = lane == j ? m : my_key;
+            };
+            for (int j = 0; j < k; ++j) round(j);
+            if (exact) break;
+            // ---- one more to see that the last one was clear, and more as long as it is not
+            const int pool = G > 1 ? r.topk_groups * n : E;           // candidates there were
+            int count = k;
+            if (count == 32 && pool > 32) continue;                   // no lane for the one after
+            if (pool > count) round(count++);
+            const float mine = route_unkey(my_key);
+            const float down = __shfl_down_sync(kAll, mine, 1);
+            bool doubt = lane + 1 < count && !(mine - down > key_margin(margin, fmaxf(fabsf(mine), fabsf(down))));
+            if (!__any_sync(kAll, doubt)) break;
+            // equal logits with equal biases have equal keys: the lower index came first
+            const int next_e = __shfl_down_sync(kAll, sel_e, 1);
+            doubt = doubt && !(__ldg(row + sel_e) == __ldg(row + next_e) &&
+                               (!bias || __ldg(bias + sel_e) == __ldg(bias + next_e)));
+            if (!__any_sync(kAll, doubt)) break;
+            bool clear;                                               // the last winner is clearly below the others
+            for (;;) {
+                const float a = route_unkey(__shfl_sync(kAll, my_key, count - 2)), c = route_unkey(__shfl_sync(kAll, my_key, count - 1));
+                clear = count > k && a - c > key_margin(margin, fmaxf(fabsf(a), fabsf(c)));
+                if (clear || count >= pool || count == 32) break;
+                round(count++);
             }
-            if (sure) break;
+            if (!clear && count < pool) continue;                     // too many near one another
+            sel_e = exact_order(row, bias, E, softmax, top, sel_e, clear ? count - 1 : count, lane);
+            break;
         }
         // ---- weights, from the selected logits
+        const float sel_x = lane < k ? __ldg(row + sel_e) : 0.f;
         float p;
         if (softmax) {
             const float m = r.renorm ? warp_max(lane < k ? sel_x : -INFINITY) : top;
@@ -249,11 +363,81 @@ route_grouped_kernel(int T, int E, int k, const moe_router r, const float* __res
 // with p the renormalised scores.  The differences g_j - g_i stand for g_j - sum_i p_i g_i,
 // which cancels when one expert dominates.  For the same reason the last form is taken as
 // g_j (1 - s_j) - sum_{i != j} s_i g_i with 1 - s of the largest logit summed without it.
-template <bool DENSE>
+//
+// The last form takes a warp a token.  The others take G lanes a token (the power of two at
+// or above k): 32 / G tokens a warp zero their rows together, then lane j of a token writes
+// its j-th expert's gradient.  An id out of range or repeated inside the token (the first
+// stays valid, as in the dispatch) takes no part and raises the status.
+// Bound by writing the rows (16384 x 256, k = 8: BWD_LARGE us; a warp a token: 9.4).
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+    return v;
+}
+template <int G>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
+    return v;
+}
+
+template <int G>
 __global__ void __launch_bounds__(256)
 route_grouped_grad_kernel(int T, int E, int k, const moe_router r, const float* __restrict__ logits,
                           const int32_t* __restrict__ ids, const float* __restrict__ dw, float* __restrict__ dlogits,
                           WsHeader* hdr) {
+    constexpr int TPW = 32 / G;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, j = lane % G, first = lane - j;
+    const unsigned mates = (G == 32 ? kAll : ((1u << (G & 31)) - 1u)) << first;
+    const int gwarp = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+    const int nwarps = (int)((gridDim.x * blockDim.x) >> 5);
+    const bool softmax = r.score == MOE_SCORE_SOFTMAX;
+    const int nt = (T - 1) / TPW + 1;
+    for (int wt = gwarp; wt < nt; wt += nwarps) {
+        const int t0 = wt * TPW, t = t0 + lane / G;
+        const bool mine = t < T && j < k;
+        const size_t at = (size_t)t * k + j;
+        const int id = mine ? ids[at] : -1 - lane;
+        const unsigned same = __match_any_sync(kAll, id) & mates;
+        const bool ok = mine && id >= 0 && id < E && (__ffs(same) - 1) == lane;
+        if (mine && !ok) raise_status(hdr, MOE_ERR_INVALID_ROUTE);
+        const float g = ok ? dw[at] : 0.f;
+        const float l = ok ? logits[(size_t)t * E + id] : -INFINITY;
+        float* rows = dlogits + (size_t)t0 * E;
+        const long long n = (long long)min(TPW, T - t0) * E;
+        if (E % 4 == 0) {
+            for (long long i = lane; i < n / 4; i += 32) reinterpret_cast<float4*>(rows)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+            for (long long i = lane; i < n; i += 32) rows[i] = 0.f;
+        }
+        // s = e^lo / (1 + em), 1 - s = q; the largest lo drops out of renormalised scores
+        const float lo = softmax ? l : fminf(l, 0.f);
+        const float em = softmax ? 0.f : expf(-fabsf(l));
+        const float m = r.renorm ? lanes_max<G>(ok ? lo : -INFINITY) : 0.f;
+        float p = ok ? expf(lo - m) / (1.0f + em) : 0.f;
+        const float q = softmax ? 1.0f : (l > 0.f ? em : 1.0f) / (1.0f + em);
+        float d = g;
+        if (r.renorm) {
+            p = p / lanes_sum<G>(p);
+            d = 0.f;
+            for (int i = 0; i < k; ++i) {
+                const float pi = __shfl_sync(kAll, p, first + i), gi = __shfl_sync(kAll, g, first + i);
+                d = fmaf(pi, g - gi, d);
+            }
+        }
+        __syncwarp();                                  // the zeros come before the selected entries
+        if (ok) rows[(size_t)(t - t0) * E + id] = r.scale * (p * q) * d;
+    }
+}
+
+// Softmax scores as they are: the gradient of every logit.
+__global__ void __launch_bounds__(256)
+route_dense_grad_kernel(int T, int E, int k, const moe_router r, const float* __restrict__ logits,
+                        const int32_t* __restrict__ ids, const float* __restrict__ dw, float* __restrict__ dlogits,
+                        WsHeader* hdr) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
@@ -268,75 +452,57 @@ route_grouped_grad_kernel(int T, int E, int k, const moe_router r, const float* 
         if (lane < k && !ok) raise_status(hdr, MOE_ERR_INVALID_ROUTE);
         const float g = ok ? dw[(size_t)t * k + lane] : 0.f;
         const float l = ok ? row[id] : -INFINITY;
-        float d;
-        if (DENSE) {
-            float m = -INFINITY;
-            int at = 0;
-            for (int e = lane; e < E; e += 32)
-                if (row[e] > m) { m = row[e]; at = e; }
-            const float top = warp_max(m);
-            at = (int)__reduce_min_sync(kAll, m == top ? (unsigned)at : 0xffffffffu);
-            float rest = 0.f;                                   // of the normaliser, without its largest term
-            for (int e = lane; e < E; e += 32) rest += e == at ? 0.f : expf(row[e] - top);
-            rest = warp_sum(rest);
-            const float iz = 1.0f / (1.0f + rest);
-            const float s = ok ? expf(l - top) * iz : 0.f;
-            const float sg = s * g;
-            const float a = warp_sum(sg);
-            float others = 0.f;
-            for (int i = 0; i < k; ++i) {
-                const float o = __shfl_sync(kAll, sg, i);
-                others += i == lane ? 0.f : o;
-            }
-            d = r.scale * s * (g * (id == at ? rest * iz : 1.0f - s) - others);
-            const float f = -r.scale * a * iz;
-            for (int e = lane; e < E; e += 32) out[e] = f * expf(row[e] - top);
-        } else {
-            if (E % 4 == 0) {
-                for (int i = lane; i < E / 4; i += 32) reinterpret_cast<float4*>(out)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            } else {
-                for (int i = lane; i < E; i += 32) out[i] = 0.f;
-            }
-            const bool softmax = r.score == MOE_SCORE_SOFTMAX;
-            const float lo = softmax ? l : fminf(l, 0.f);
-            const float em = softmax ? 0.f : expf(-fabsf(l));           // 1 - s = 1/(1+e^l)
-            const float m = r.renorm ? warp_max(ok ? lo : -INFINITY) : 0.f;
-            float p = ok ? expf(lo - m) / (1.0f + em) : 0.f;
-            const float q = softmax ? 1.0f : (l > 0.f ? em : 1.0f) / (1.0f + em);
-            if (r.renorm) {
-                p = p / warp_sum(p);
-                float s = 0.f;
-                for (int i = 0; i < k; ++i) {
-                    const float pi = __shfl_sync(kAll, p, i), gi = __shfl_sync(kAll, g, i);
-                    s = fmaf(pi, g - gi, s);
-                }
-                d = r.scale * (p * q) * s;
-            } else {
-                d = r.scale * (p * q) * g;
-            }
+        float m = -INFINITY;
+        int at = 0;
+        for (int e = lane; e < E; e += 32)
+            if (row[e] > m) { m = row[e]; at = e; }
+        const float top = warp_max(m);
+        at = (int)__reduce_min_sync(kAll, m == top ? (unsigned)at : 0xffffffffu);
+        float rest = 0.f;                                   // of the normaliser, without its largest term
+        for (int e = lane; e < E; e += 32) rest += e == at ? 0.f : expf(row[e] - top);
+        rest = warp_sum(rest);
+        const float iz = 1.0f / (1.0f + rest);
+        const float s = ok ? expf(l - top) * iz : 0.f;
+        const float sg = s * g;
+        const float a = warp_sum(sg);
+        float others = 0.f;
+        for (int i = 0; i < k; ++i) {
+            const float o = __shfl_sync(kAll, sg, i);
+            others += i == lane ? 0.f : o;
         }
+        const float f = -r.scale * a * iz;
+        for (int e = lane; e < E; e += 32) out[e] = f * expf(row[e] - top);
         __syncwarp();                                  // the row comes before the selected entries
-        if (ok) out[id] = d;
+        if (ok) out[id] = r.scale * s * (g * (id == at ? rest * iz : 1.0f - s) - others);
     }
 }
 
-unsigned warps_grid(int tokens) {
-    long long blocks = ((long long)tokens + 7) / 8;
+unsigned warps_grid(long long warps) {
+    const long long blocks = (warps + 7) / 8;
     const long long cap = (long long)device_sm_count() * 8;
     return (unsigned)(blocks < cap ? blocks : cap);
 }
 
-template <int EPL>
+template <int EPL, bool FULL>
 cudaError_t launch_epl(const moe_shape& s, const moe_router& r, const float* logits, const float* bias, int32_t* ids,
                        float* w, WsHeader* hdr, cudaStream_t st) {
-    size_t smem = 0;
-    if (r.groups > 1) {
-        int pow2 = 1;
-        while (pow2 < r.groups) pow2 *= 2;
-        smem = (size_t)8 * (s.experts + r.groups * (32 / pow2)) * sizeof(float);
-    }
-    return launch_kernel(route_grouped_kernel<EPL>, dim3(warps_grid(s.tokens)), dim3(256), smem, st, 1, kUsePdl,
-                         s.tokens, s.experts, s.top_k, r, logits, bias, ids, w, hdr);
+    // a warp's keys: padded by 32 / pow2 lanes' worth per group, see the kernel
+    int pow2 = 1;
+    while (pow2 < r.groups) pow2 *= 2;
+    const size_t smem = (size_t)8 * (s.experts + (r.groups > 1 ? r.groups * (32 / pow2) : 32)) * sizeof(float);
+    // as many blocks as run at once: what a warp sets up serves all its tokens
+    long long blocks = ((long long)s.tokens + 7) / 8;
+    const long long cap = (long long)device_sm_count() * (EPL <= 8 ? 3 : 1);
+    if (blocks > cap) blocks = cap;
+    return launch_kernel(route_grouped_kernel<EPL, FULL>, dim3((unsigned)blocks), dim3(256), smem, st, 1, kUsePdl, s.tokens,
+                         s.experts, s.top_k, r, logits, bias, ids, w, hdr);
+}
+
+template <int EPL>
+cudaError_t launch_full(const moe_shape& s, const moe_router& r, const float* logits, const float* bias, int32_t* ids,
+                        float* w, WsHeader* hdr, cudaStream_t st) {
+    return s.experts == 32 * EPL ? launch_epl<EPL, true>(s, r, logits, bias, ids, w, hdr, st)
+                                 : launch_epl<EPL, false>(s, r, logits, bias, ids, w, hdr, st);
 }
 
 }  // namespace
@@ -344,20 +510,26 @@ cudaError_t launch_epl(const moe_shape& s, const moe_router& r, const float* log
 cudaError_t launch_route_grouped(const moe_shape& s, const moe_router& r, const float* logits, const float* bias,
                                  int32_t* ids, float* w, WsHeader* hdr, cudaStream_t st) {
     const int E = s.experts;
-    if (E <= 32) return launch_epl<1>(s, r, logits, bias, ids, w, hdr, st);
-    if (E <= 64) return launch_epl<2>(s, r, logits, bias, ids, w, hdr, st);
-    if (E <= 128) return launch_epl<4>(s, r, logits, bias, ids, w, hdr, st);
-    if (E <= 256) return launch_epl<8>(s, r, logits, bias, ids, w, hdr, st);
-    if (E <= 512) return launch_epl<16>(s, r, logits, bias, ids, w, hdr, st);
-    return launch_epl<32>(s, r, logits, bias, ids, w, hdr, st);
+    if (E <= 32) return launch_full<1>(s, r, logits, bias, ids, w, hdr, st);
+    if (E <= 64) return launch_full<2>(s, r, logits, bias, ids, w, hdr, st);
+    if (E <= 128) return launch_full<4>(s, r, logits, bias, ids, w, hdr, st);
+    if (E <= 256) return launch_full<8>(s, r, logits, bias, ids, w, hdr, st);
+    if (E <= 512) return launch_full<16>(s, r, logits, bias, ids, w, hdr, st);
+    return launch_full<32>(s, r, logits, bias, ids, w, hdr, st);
 }
 
 cudaError_t launch_route_grouped_grad(const moe_shape& s, const moe_router& r, const float* logits, const int32_t* ids,
                                       const float* dw, float* dlogits, WsHeader* hdr, cudaStream_t st) {
-    const bool dense = r.score == MOE_SCORE_SOFTMAX && !r.renorm;
-    return launch_kernel(dense ? route_grouped_grad_kernel<true> : route_grouped_grad_kernel<false>,
-                         dim3(warps_grid(s.tokens)), dim3(256), 0, st, 1, kUsePdl, s.tokens, s.experts, s.top_k, r,
-                         logits, ids, dw, dlogits, hdr);
+    auto go = [&](auto* kernel, int lanes) {
+        return launch_kernel(kernel, dim3(warps_grid(((long long)s.tokens * lanes + 31) / 32)), dim3(256), 0, st, 1, kUsePdl,
+                             s.tokens, s.experts, s.top_k, r, logits, ids, dw, dlogits, hdr);
+    };
+    if (r.score == MOE_SCORE_SOFTMAX && !r.renorm) return go(route_dense_grad_kernel, 32);
+    if (s.top_k <= 2) return go(route_grouped_grad_kernel<2>, 2);
+    if (s.top_k <= 4) return go(route_grouped_grad_kernel<4>, 4);
+    if (s.top_k <= 8) return go(route_grouped_grad_kernel<8>, 8);
+    if (s.top_k <= 16) return go(route_grouped_grad_kernel<16>, 16);
+    return go(route_grouped_grad_kernel<32>, 32);
 }
 
 }  // namespace moe

@@ -565,22 +565,27 @@ def fp8_blocks(n: int) -> int:
     return (n + FP8_BLOCK - 1) // FP8_BLOCK
 
 
-def _on(t, dtypes, n, what):
-    """The address of a contiguous tensor of the current device with `n` elements at least of
-    one of `dtypes`; None and plain addresses pass as they are."""
+def _device() -> int:
+    """The current device (0 where there is none: the calls then refuse every tensor)."""
     try:
-        if t.dtype in dtypes and t.numel() >= n and t.is_cuda and t.is_contiguous() and \
-                t.get_device() == torch._C._cuda_getDevice():
+        return torch._C._cuda_getDevice()
+    except RuntimeError:
+        return 0
+
+
+def _on(t, dtypes, n, what, dev):
+    """The address of a contiguous tensor of device `dev` with `n` elements at least of one of
+    `dtypes`; None and plain addresses pass as they are."""
+    try:
+        if t.dtype in dtypes and t.numel() >= n and t.get_device() == dev and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         return _ptr(t)
     if t.dtype not in dtypes or t.numel() < n:
         raise ValueError(f"{what}: {' or '.join(map(str, dtypes))} with {n} elements at least expected, "
                          f"got {t.dtype} {tuple(t.shape)}")
-    p = _ptr(t)
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{what}: a tensor of {t.device}, the current device is {torch._C._cuda_getDevice()}")
-    return p
+    _ptr(t)
+    raise ValueError(f"{what}: a tensor of {t.device}, the current device is cuda:{dev}")
 
 
 _B, _F, _I, _C, _U = (_BF16,), (_F32,), (_I32,), _CODES, (torch.uint8,)
@@ -608,22 +613,22 @@ def _fp8_counts(fields: bytes) -> _Fp8Counts:
 
 def moe_route_grouped(shape, router, logits, bias, topk_ids, topk_w, ws, stream=None):
     """Group-limited top-k routing of float32 logits; `bias` (or None) only selects."""
-    n = _counts_of(bytes(shape))
-    st = (_lib or lib()).moe_route_grouped(shape, router, _on(logits, _F, n.logits, "logits"),
-                                           _on(bias, _F, shape.experts, "bias"),
-                                           _on(topk_ids, _I, n.pairs, "topk_ids"), _on(topk_w, _F, n.pairs, "topk_w"),
-                                           _on(ws, _U, 0, "ws"), _wsb(ws), _stream(stream))
+    n, dev = _counts_of(bytes(shape)), _device()
+    st = (_lib or lib()).moe_route_grouped(shape, router, _on(logits, _F, n.logits, "logits", dev),
+                                           _on(bias, _F, shape.experts, "bias", dev),
+                                           _on(topk_ids, _I, n.pairs, "topk_ids", dev), _on(topk_w, _F, n.pairs, "topk_w", dev),
+                                           _on(ws, _U, 0, "ws", dev), _wsb(ws), _stream(stream))
     if st:
         raise MoEError(st, "moe_route_grouped")
 
 
 def moe_route_grouped_backward(shape, router, logits, topk_ids, dtopk_w, dlogits, ws, stream=None):
     """Gradient of moe_route_grouped's weights in the logits, for the selection topk_ids."""
-    n = _counts_of(bytes(shape))
-    st = (_lib or lib()).moe_route_grouped_backward(shape, router, _on(logits, _F, n.logits, "logits"),
-                                                    _on(topk_ids, _I, n.pairs, "topk_ids"),
-                                                    _on(dtopk_w, _F, n.pairs, "dtopk_w"),
-                                                    _on(dlogits, _F, n.logits, "dlogits"), _on(ws, _U, 0, "ws"),
+    n, dev = _counts_of(bytes(shape)), _device()
+    st = (_lib or lib()).moe_route_grouped_backward(shape, router, _on(logits, _F, n.logits, "logits", dev),
+                                                    _on(topk_ids, _I, n.pairs, "topk_ids", dev),
+                                                    _on(dtopk_w, _F, n.pairs, "dtopk_w", dev),
+                                                    _on(dlogits, _F, n.logits, "dlogits", dev), _on(ws, _U, 0, "ws", dev),
                                                     _wsb(ws), _stream(stream))
     if st:
         raise MoEError(st, "moe_route_grouped_backward")
@@ -632,13 +637,13 @@ def moe_route_grouped_backward(shape, router, logits, topk_ids, dtopk_w, dlogits
 def moe_dispatch_fp8_block(shape, x, topk_ids, counts, offsets, dest, sorted_pair, x_perm, x_scale, ws, stream=None):
     """moe_dispatch with the rows quantized: x_perm E4M3 codes (uint8 or float8_e4m3fn) [T*k, H],
     x_scale float32 [T*k, ceil(H / 128)]."""
-    n, m = _counts_of(bytes(shape)), _fp8_counts(bytes(shape))
-    st = (_lib or lib()).moe_dispatch_fp8_block(shape, _on(x, _B, n.x, "x"), _on(topk_ids, _I, n.pairs, "topk_ids"),
-                                                _on(counts, _I, shape.experts, "counts"),
-                                                _on(offsets, _I, n.bounds, "offsets"), _on(dest, _I, n.pairs, "dest"),
-                                                _on(sorted_pair, _I, n.pairs, "sorted_pair"),
-                                                _on(x_perm, _C, m.x_perm, "x_perm"),
-                                                _on(x_scale, _F, m.x_scale, "x_scale"), _on(ws, _U, 0, "ws"), _wsb(ws),
+    n, m, dev = _counts_of(bytes(shape)), _fp8_counts(bytes(shape)), _device()
+    st = (_lib or lib()).moe_dispatch_fp8_block(shape, _on(x, _B, n.x, "x", dev), _on(topk_ids, _I, n.pairs, "topk_ids", dev),
+                                                _on(counts, _I, shape.experts, "counts", dev),
+                                                _on(offsets, _I, n.bounds, "offsets", dev), _on(dest, _I, n.pairs, "dest", dev),
+                                                _on(sorted_pair, _I, n.pairs, "sorted_pair", dev),
+                                                _on(x_perm, _C, m.x_perm, "x_perm", dev),
+                                                _on(x_scale, _F, m.x_scale, "x_scale", dev), _on(ws, _U, 0, "ws", dev), _wsb(ws),
                                                 _stream(stream))
     if st:
         raise MoEError(st, "moe_dispatch_fp8_block")
@@ -646,12 +651,12 @@ def moe_dispatch_fp8_block(shape, x, topk_ids, counts, offsets, dest, sorted_pai
 
 def moe_expert_up_fp8_block(shape, x_perm, x_scale, offsets, w13, w13_scale, h, h_scale, ws, stream=None):
     """Up projection and activation in block-scaled FP8, quantized again into h and h_scale."""
-    n, m = _counts_of(bytes(shape)), _fp8_counts(bytes(shape))
-    st = (_lib or lib()).moe_expert_up_fp8_block(shape, _on(x_perm, _C, m.x_perm, "x_perm"),
-                                                 _on(x_scale, _F, m.x_scale, "x_scale"),
-                                                 _on(offsets, _I, n.bounds, "offsets"), _on(w13, _C, m.w13, "w13"),
-                                                 _on(w13_scale, _F, m.w13_scale, "w13_scale"), _on(h, _C, m.h, "h"),
-                                                 _on(h_scale, _F, m.h_scale, "h_scale"), _on(ws, _U, 0, "ws"),
+    n, m, dev = _counts_of(bytes(shape)), _fp8_counts(bytes(shape)), _device()
+    st = (_lib or lib()).moe_expert_up_fp8_block(shape, _on(x_perm, _C, m.x_perm, "x_perm", dev),
+                                                 _on(x_scale, _F, m.x_scale, "x_scale", dev),
+                                                 _on(offsets, _I, n.bounds, "offsets", dev), _on(w13, _C, m.w13, "w13", dev),
+                                                 _on(w13_scale, _F, m.w13_scale, "w13_scale", dev), _on(h, _C, m.h, "h", dev),
+                                                 _on(h_scale, _F, m.h_scale, "h_scale", dev), _on(ws, _U, 0, "ws", dev),
                                                  _wsb(ws), _stream(stream))
     if st:
         raise MoEError(st, "moe_expert_up_fp8_block")
@@ -659,11 +664,11 @@ def moe_expert_up_fp8_block(shape, x_perm, x_scale, offsets, w13, w13_scale, h, 
 
 def moe_expert_down_fp8_block(shape, h, h_scale, offsets, w2, w2_scale, y_perm, ws, stream=None):
     """Down projection in block-scaled FP8 into y_perm (bfloat16)."""
-    n, m = _counts_of(bytes(shape)), _fp8_counts(bytes(shape))
-    st = (_lib or lib()).moe_expert_down_fp8_block(shape, _on(h, _C, m.h, "h"), _on(h_scale, _F, m.h_scale, "h_scale"),
-                                                   _on(offsets, _I, n.bounds, "offsets"), _on(w2, _C, m.w2, "w2"),
-                                                   _on(w2_scale, _F, m.w2_scale, "w2_scale"),
-                                                   _on(y_perm, _B, n.rows, "y_perm"), _on(ws, _U, 0, "ws"), _wsb(ws),
+    n, m, dev = _counts_of(bytes(shape)), _fp8_counts(bytes(shape)), _device()
+    st = (_lib or lib()).moe_expert_down_fp8_block(shape, _on(h, _C, m.h, "h", dev), _on(h_scale, _F, m.h_scale, "h_scale", dev),
+                                                   _on(offsets, _I, n.bounds, "offsets", dev), _on(w2, _C, m.w2, "w2", dev),
+                                                   _on(w2_scale, _F, m.w2_scale, "w2_scale", dev),
+                                                   _on(y_perm, _B, n.rows, "y_perm", dev), _on(ws, _U, 0, "ws", dev), _wsb(ws),
                                                    _stream(stream))
     if st:
         raise MoEError(st, "moe_expert_down_fp8_block")
@@ -672,14 +677,14 @@ def moe_expert_down_fp8_block(shape, h, h_scale, offsets, w2, w2_scale, y_perm, 
 def moe_layer_fp8_block(shape, logits, ids_in, w_in, x, w13, w13_scale, w2, w2_scale, out, ws, stream=None,
                         residual=None):
     """The layer with block-scaled FP8 experts (no shared experts)."""
-    n, m = _counts_of(bytes(shape)), _fp8_counts(bytes(shape))
-    st = (_lib or lib()).moe_layer_fp8_block(shape, _on(logits, _F, n.logits, "logits"),
-                                             _on(ids_in, _I, n.pairs, "ids_in"), _on(w_in, _F, n.pairs, "w_in"),
-                                             _on(x, _B, n.x, "x"), _on(w13, _C, m.w13, "w13"),
-                                             _on(w13_scale, _F, m.w13_scale, "w13_scale"), _on(w2, _C, m.w2, "w2"),
-                                             _on(w2_scale, _F, m.w2_scale, "w2_scale"),
-                                             _on(residual, _B, n.x, "residual"), _on(out, _B, n.x, "out"),
-                                             _on(ws, _U, 0, "ws"), _wsb(ws), _stream(stream))
+    n, m, dev = _counts_of(bytes(shape)), _fp8_counts(bytes(shape)), _device()
+    st = (_lib or lib()).moe_layer_fp8_block(shape, _on(logits, _F, n.logits, "logits", dev),
+                                             _on(ids_in, _I, n.pairs, "ids_in", dev), _on(w_in, _F, n.pairs, "w_in", dev),
+                                             _on(x, _B, n.x, "x", dev), _on(w13, _C, m.w13, "w13", dev),
+                                             _on(w13_scale, _F, m.w13_scale, "w13_scale", dev), _on(w2, _C, m.w2, "w2", dev),
+                                             _on(w2_scale, _F, m.w2_scale, "w2_scale", dev),
+                                             _on(residual, _B, n.x, "residual", dev), _on(out, _B, n.x, "out", dev),
+                                             _on(ws, _U, 0, "ws", dev), _wsb(ws), _stream(stream))
     if st:
         raise MoEError(st, "moe_layer_fp8_block")
 

@@ -34,7 +34,9 @@ def rows_of(g, R, H):
 # ---- quantizing dispatch -----------------------------------------------------------
 #         T    H     E   k
 SIZES = [(1, 16, 1, 1), (1, 7168, 16, 8), (3, 48, 4, 2), (37, 144, 33, 5), (64, 256, 16, 2), (40, 1040, 8, 8),
-         (300, 128, 1024, 32), (700, 2048, 64, 6), (3, 20000, 6, 3), (16, 1008, 9, 3)]
+         (300, 128, 1024, 32), (700, 2048, 64, 6), (3, 20000, 6, 3), (16, 1008, 9, 3),
+         # one launch up to 12288 pairs, three from there on
+         (1365, 64, 40, 9), (1366, 64, 40, 9), (384, 32, 64, 32), (385, 32, 64, 32), (12288, 16, 5, 1), (2400, 272, 300, 8)]
 
 
 def dispatch_buffers(T, H, E, k):
