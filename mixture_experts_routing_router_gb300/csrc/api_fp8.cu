@@ -75,12 +75,14 @@ moe_status do_up(const moe_shape& s, const uint8_t* x_perm, const float* x_scale
     g.w = w13; g.w_scale = w13_scale;
     g.K = s.hidden; g.N = s.inter;
     g.out = h; g.out_scale = h_scale;
+    g.max_group_rows = s.tokens;                   // a token's experts are distinct
     g.gated = gated;
     return launch_fp8_gemm(g, at<WsHeader>(ws, 0), st);
 }
 
 moe_status do_down(const moe_shape& s, const uint8_t* h, const float* h_scale, const int32_t* offsets,
-                   const uint8_t* w2, const float* w2_scale, uint16_t* y_perm, void* ws, cudaStream_t st, int gated) {
+                   const uint8_t* w2, const float* w2_scale, uint16_t* y_perm, void* ws, cudaStream_t st, int gated,
+                   int early) {
     Fp8Problem g{};
     g.mode = kGemmPlain;
     g.a = h; g.a_scale = h_scale; g.rows = (long long)s.tokens * s.top_k;
@@ -88,6 +90,8 @@ moe_status do_down(const moe_shape& s, const uint8_t* h, const float* h_scale, c
     g.w = w2; g.w_scale = w2_scale;
     g.K = s.inter; g.N = s.hidden;
     g.out = y_perm;
+    g.early = early;
+    g.max_group_rows = s.tokens;                   // a token's experts are distinct
     g.gated = gated;
     return launch_fp8_gemm(g, at<WsHeader>(ws, 0), st);
 }
@@ -156,7 +160,7 @@ moe_status moe_expert_down_fp8_block(const moe_shape* shape, const uint8_t* h, c
     if (!aligned(h, 16) || !aligned(h_scale, 16) || !aligned(offsets, 16) || !aligned(w2, 16) ||
         !aligned(w2_scale, 16) || !aligned(y_perm, 16))
         return MOE_ERR_INVALID_ARG;
-    return do_down(*shape, h, h_scale, offsets, w2, w2_scale, y_perm, ws, static_cast<cudaStream_t>(stream), 0);
+    return do_down(*shape, h, h_scale, offsets, w2, w2_scale, y_perm, ws, static_cast<cudaStream_t>(stream), 0, 0);
 }
 
 moe_status moe_layer_fp8_block(const moe_shape* shape, const float* logits, const int32_t* ids_in, const float* w_in,
@@ -197,7 +201,7 @@ moe_status moe_layer_fp8_block(const moe_shape* shape, const float* logits, cons
                          x_scale, ws, st)) != MOE_OK)
         return r;
     if ((r = do_up(s, x_perm, x_scale, offsets, w13, w13_scale, h, h_scale, ws, st, 1)) != MOE_OK) return r;
-    if ((r = do_down(s, h, h_scale, offsets, w2, w2_scale, y_perm, ws, st, 1)) != MOE_OK) return r;
+    if ((r = do_down(s, h, h_scale, offsets, w2, w2_scale, y_perm, ws, st, 1, 1)) != MOE_OK) return r;
     return from_cuda(launch_combine(s, y_perm, dest, w, nullptr, residual, out, hdr, st));
 }
 

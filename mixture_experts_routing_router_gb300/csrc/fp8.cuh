@@ -64,7 +64,9 @@ struct Fp8Problem {
     const uint8_t* w; const float* w_scale;    // [groups, parts, N, K], [groups, parts, ceil(N / 128), ceil(K / 128)]
     int K, N;
     void* out; float* out_scale;               // plain: bf16 [rows, N]; else E4M3 [rows, N], [rows, ceil(N / 128)]
+    int max_group_rows;                        // host bound on the rows of a group
     int gated;                                 // as GemmProblem
+    int early;                                 // 1: the bucket bounds are final when the kernel starts
 };
 moe_status launch_fp8_gemm(const Fp8Problem& p, WsHeader* hdr, cudaStream_t st);
 

@@ -28,18 +28,15 @@
 // Persistent CTAs walk a tile list built from the bucket bounds, as in gemm.cu.  Every
 // wait is bounded (MOE_ERR_TIMEOUT); the exchange goes through an mbarrier so that it is,
 // too.
-#include "fp8.cuh"
+#include "gemm_fp8.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int F_BM = 128;                       // activation rows per tile
-constexpr int F_BOX = 128 * 128;                // 128 rows of 128 codes
 constexpr int F_THREADS = 384;
 constexpr int F_EPI_WARPS = 8;
-constexpr int F_MAX_SMEM = 227 * 1024;
 constexpr int F_STORE = 2048;                   // shared memory of a warp's output: 32 rows of 64 bytes
-constexpr int F_RASTER = 8;                     // column tiles of a band (tile order)
 
 template <int NSUB>
 struct FCfg {
@@ -49,20 +46,6 @@ struct FCfg {
     static constexpr int ACCS = 512 / ACC_COLS;
 };
 
-struct FParams {
-    const int32_t* offsets;
-    int groups, rows;
-    int K, N, nkb, nnb;                         // nkb, nnb: 128-blocks of K and of N
-    int parts;                                  // weight matrices per group (SwiGLU: gate and up)
-    int ntn;                                    // column tiles
-    const float* a_scale;
-    const float* w_scale;
-    void* out;
-    float* out_scale;
-    WsHeader* hdr;
-    int gated;
-};
-
 struct FCtl {
     unsigned long long full[6], empty[6];
     unsigned long long tfull[4], tempty[4];
@@ -70,57 +53,9 @@ struct FCtl {
     unsigned long long drain;
     uint32_t tmem_base;
     int abort;
-    int total;
     int wtot[F_THREADS / 32];
     float amax[2][2][2][F_BM];                  // [exchange parity][block][column half][row]
 };
-
-__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
-}
-// kind::f8f6f4: E4M3 A and B (both K-major), FP32 D, M x N.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ unsigned long long pack_f32x2(float lo, float hi) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack_f32x2(unsigned long long v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ unsigned long long fma_f32x2(unsigned long long a, unsigned long long b, unsigned long long c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-// 64 consecutive FP32 columns of this warp's 32 TMEM lanes as 32 pairs, waited for (load
-// and wait in one statement: no use of the registers can come before the wait).
-__device__ __forceinline__ void tmem_ld_pairs64(uint32_t taddr, unsigned long long (&r)[32]) {
-    asm volatile("{\n\t.reg .b32 t<64>;\n\ttcgen05.ld.sync.aligned.32x32b.x64.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31,t32,t33,t34,t35,t36,t37,t38,t39,t40,t41,t42,t43,t44,t45,t46,t47,t48,t49,t50,t51,t52,t53,t54,t55,t56,t57,t58,t59,t60,t61,t62,t63}, [%32];\n\ttcgen05.wait::ld.sync.aligned;\n\tmov.b64 %0, {t0,t1};\n\tmov.b64 %1, {t2,t3};\n\tmov.b64 %2, {t4,t5};\n\tmov.b64 %3, {t6,t7};\n\tmov.b64 %4, {t8,t9};\n\tmov.b64 %5, {t10,t11};\n\tmov.b64 %6, {t12,t13};\n\tmov.b64 %7, {t14,t15};\n\tmov.b64 %8, {t16,t17};\n\tmov.b64 %9, {t18,t19};\n\tmov.b64 %10, {t20,t21};\n\tmov.b64 %11, {t22,t23};\n\tmov.b64 %12, {t24,t25};\n\tmov.b64 %13, {t26,t27};\n\tmov.b64 %14, {t28,t29};\n\tmov.b64 %15, {t30,t31};\n\tmov.b64 %16, {t32,t33};\n\tmov.b64 %17, {t34,t35};\n\tmov.b64 %18, {t36,t37};\n\tmov.b64 %19, {t38,t39};\n\tmov.b64 %20, {t40,t41};\n\tmov.b64 %21, {t42,t43};\n\tmov.b64 %22, {t44,t45};\n\tmov.b64 %23, {t46,t47};\n\tmov.b64 %24, {t48,t49};\n\tmov.b64 %25, {t50,t51};\n\tmov.b64 %26, {t52,t53};\n\tmov.b64 %27, {t54,t55};\n\tmov.b64 %28, {t56,t57};\n\tmov.b64 %29, {t58,t59};\n\tmov.b64 %30, {t60,t61};\n\tmov.b64 %31, {t62,t63};\n\t}" : "=l"(r[0]),"=l"(r[1]),"=l"(r[2]),"=l"(r[3]),"=l"(r[4]),"=l"(r[5]),"=l"(r[6]),"=l"(r[7]),"=l"(r[8]),"=l"(r[9]),"=l"(r[10]),"=l"(r[11]),"=l"(r[12]),"=l"(r[13]),"=l"(r[14]),"=l"(r[15]),"=l"(r[16]),"=l"(r[17]),"=l"(r[18]),"=l"(r[19]),"=l"(r[20]),"=l"(r[21]),"=l"(r[22]),"=l"(r[23]),"=l"(r[24]),"=l"(r[25]),"=l"(r[26]),"=l"(r[27]),"=l"(r[28]),"=l"(r[29]),"=l"(r[30]),"=l"(r[31]) : "r"(taddr) : "memory");
-}
-
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Four steps' scales for a warp, copied while the four before are used: float [32 rows][4]
 // and float [2 blocks][4].
@@ -129,47 +64,6 @@ struct FScales {
     float w[2][4];
 };
 static_assert(2 * sizeof(FScales) <= F_STORE && sizeof(FScales) % 16 == 0, "two of them in a warp's output buffer");
-
-// 1 / (1 + e^-x): two of the approximate units' operations, 2^-21 of the value for |x| < 8
-// (e^-x overflows to infinity where the result is 0 to FP32's normal range).
-__device__ __forceinline__ float sigmoid_approx(float x) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return r;
-}
-
-struct FTile { int g, nt, row0, rows; };        // first row of the tile and how many it holds
-
-// The tile list: group g's row tiles times column tiles, in bands of F_RASTER column
-// tiles.  The up projection (long rows) walks a band's column tiles first, the down
-// projection its row tiles (as gemm.cu, for the same reuse in L2).
-// `lo`: a group at or before the tile's (that of the role's last tile: they ascend).
-template <bool COLS_FIRST>
-__device__ __forceinline__ FTile f_tile(int tile, int& lo, const int* prefix, const int* start, const FParams& p) {
-    int hi = p.groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= tile) lo = mid; else hi = mid;
-    }
-    const int cnt = start[p.groups + lo], local = tile - prefix[lo];
-    const int mtiles = (cnt + F_BM - 1) / F_BM;
-    const int band = local / (mtiles * F_RASTER), idx = local - band * mtiles * F_RASTER;
-    FTile t;
-    int mt;
-    if (COLS_FIRST) {
-        const int w = min(F_RASTER, p.ntn - band * F_RASTER);
-        mt = idx / w;
-        t.nt = band * F_RASTER + idx % w;
-    } else {
-        mt = idx % mtiles;
-        t.nt = band * F_RASTER + idx / mtiles;
-    }
-    t.g = lo;
-    t.row0 = start[lo] + mt * F_BM;
-    t.rows = min(F_BM, cnt - mt * F_BM);
-    return t;
-}
 
 // A warp's piece of the output, 64 bytes (u) of each of its 32 rows, a row per lane: turned
 // around in shared memory so that four lanes write a row's 64 bytes (straight from the
@@ -241,38 +135,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     }
     pdl_wait();
     pdl_trigger();
-    // ---- tile list: bounds clamped to the rows there are
-    const bool skip = p.gated && p.hdr->cap_exceeded;
-    const int per = (p.groups + F_THREADS - 1) / F_THREADS, g0 = tid * per;
-    int sum = 0;
-    for (int g = g0; g < min(g0 + per, p.groups); ++g) {
-        int lo = p.offsets[g], hi = p.offsets[g + 1];
-        lo = lo < 0 ? 0 : min(lo, p.rows);
-        hi = hi < lo || skip ? lo : min(hi, p.rows);
-        start[g] = lo;
-        start[p.groups + g] = hi - lo;
-        sum += ((hi - lo + F_BM - 1) / F_BM) * p.ntn;
-    }
-    int inc = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += v;
-    }
-    if (lane == 31) ctl->wtot[warp] = inc;
-    __syncthreads();
-    int run = inc - sum;
-    for (int w = 0; w < warp; ++w) run += ctl->wtot[w];
-    for (int g = g0; g < min(g0 + per, p.groups); ++g) {
-        prefix[g] = run;
-        run += ((start[p.groups + g] + F_BM - 1) / F_BM) * p.ntn;
-    }
-    if (tid == F_THREADS - 1) ctl->total = prefix[p.groups] = run;
+    const int total = f_tile_list<F_THREADS, F_BM>(p, prefix, start, ctl->wtot);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
-    const int total = ctl->total;
     volatile int* abort = &ctl->abort;
 
     if (warp < 4) {
@@ -286,7 +153,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 long long armed = 0;
                 int group = 0;
                 for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-                    const FTile t = f_tile<UP>(tile, group, prefix, start, p);
+                    const FTile t = f_tile<UP, F_BM>(tile, group, prefix, start, p);
                     const int box = f_box(t.rows), boxes = f_boxes(t.rows);
                     const uint32_t bytes = (uint32_t)(NSUB * F_BOX + boxes * box * 128);
                     const int w0 = t.g * p.parts * p.N + t.nt * BN;
@@ -376,7 +243,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if ((seen & 31) == 0) {
                 int group = 0;
                 const long long mine_at = tile + (long long)lane * gridDim.x;
-                if (mine_at < total) mytile = f_tile<UP>((int)mine_at, group, prefix, start, p);
+                if (mine_at < total) mytile = f_tile<UP, F_BM>((int)mine_at, group, prefix, start, p);
                 __syncwarp();
             }
             t.g = __shfl_sync(0xffffffffu, mytile.g, seen & 31);
@@ -390,7 +257,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const int second = MODE == kGemmSwiGLU ? p.nnb : b0 + 1 < p.nnb ? 1 : 0;
             ws = p.w_scale + ((size_t)t.g * p.parts * p.nnb + b0 + (lane < 4 ? 0 : second)) * p.nkb;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a4[i] = __ldg(as + min(i, p.nkb - 1));
+            for (int i = 0; i < 4; ++i) a4[i] = __ldcg(as + min(i, p.nkb - 1));
             if (lane < 4 * NSUB) w1 = __ldg(ws + min(lane & 3, p.nkb - 1));
         };
         auto fetch = [&](int k0) {
@@ -438,11 +305,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     const uint32_t ta = tmem + (uint32_t)(acc * C::ACC_COLS + 64 * hf) + ((uint32_t)(32 * q) << 16);
 #pragma unroll
                     for (int s = 0; s < NSUB; ++s) {
-                        unsigned long long v[32];
-                        tmem_ld_pairs64(ta + (uint32_t)(s * 128), v);
+                        uint32_t v[64];
+                        tmem_ld_cols(ta + (uint32_t)(s * 128), v);
+                        tmem_ld_wait();
+                        tmem_ld_done(v);
                         const unsigned long long ff = pack_f32x2(f[s], f[s]);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) sum[s][i] = fma_f32x2(v[i], ff, sum[s][i]);
+                        for (int i = 0; i < 32; ++i)
+                            sum[s][i] = fma_f32x2(pack_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ff, sum[s][i]);
                     }
                 }
                 tc_fence_before();
@@ -575,10 +445,12 @@ moe_status launch_fp8_gemm(const Fp8Problem& g, WsHeader* hdr, cudaStream_t st) 
     p.hdr = hdr;
     p.gated = g.gated;
     CUtensorMap ma[3], mw;
+    if (!make_tensor_map_u8_rows(&mw, g.w, (long long)g.groups * p.parts * g.N, g.K, g.K, 128u, 128u)) return MOE_ERR_CUDA;
+    if (g.max_group_rows <= 64)
+        return launch_fp8_rows(g, p, mw, g.max_group_rows <= 16 ? 16 : g.max_group_rows <= 32 ? 32 : 64, st);
     const unsigned box[3] = {128u, 32u, 8u};
     for (int i = 0; i < 3; ++i)
         if (!make_tensor_map_u8_rows(&ma[i], g.a, g.rows, g.K, g.K, 128u, box[i])) return MOE_ERR_CUDA;
-    if (!make_tensor_map_u8_rows(&mw, g.w, (long long)g.groups * p.parts * g.N, g.K, g.K, 128u, 128u)) return MOE_ERR_CUDA;
     if (g.mode == kGemmSwiGLU) return launch_f<kGemmSwiGLU, 2>(g, p, mw, ma, st);
     // Two blocks of weight rows a tile halve the activation traffic; with fewer such tiles
     // than SMs, one block a tile spreads a weight stream over twice as many.

@@ -164,6 +164,36 @@ def test_products(name, width, act):
     assert torch.all(h.t[n:] == 0x5A) and torch.all(hs.t[n:] == 7.0) and torch.all(y.t[n:].view(U8) == 0x5A)
 
 
+@pytest.mark.parametrize("act", ["swiglu", "relu2"])
+@pytest.mark.parametrize("width", [(16, 16), (144, 112), (272, 400), (1024, 640), (2064, 144), (400, 1536)], ids=str)
+@pytest.mark.parametrize("tokens", [1, 8, 9, 16, 17, 31, 33, 64])
+def test_products_of_few_rows(tokens, width, act):
+    """Few rows a group (decode): every group at most as many as there are tokens, and, with
+    bounds that no dispatch of so few tokens makes, groups that span several tiles."""
+    H, I = width
+    E, k = 12, 5
+    R, spread = tokens * k, [min(tokens, 1 + (3 * e) % 7) if e % 3 == 1 else 0 for e in range(E)]
+    for buckets in (spread, [R - 3] + [0] * (E - 2) + [2]):
+        d = problem(buckets, H, I, act, seed=H + I + tokens, extra=R - sum(buckets))
+        shape = N.make_shape(tokens, H, E, k, I, act=ACT[act])
+        ws = guarded_workspace(shape)
+        h, hs, y = Guarded((R, I), U8), Guarded((R, ref.blocks(I)), F32), Guarded((R, H), BF16)
+        for o in (h, y):
+            o.t.view(U8).fill_(0x5A)
+        hs.t.fill_(7.0)
+        N.moe_expert_up_fp8_block(shape, d["x"], d["x_scale"], d["offsets"], d["w13"], d["w13_scale"], h.t, hs.t, ws.t)
+        N.moe_expert_down_fp8_block(shape, h.t, hs.t, d["offsets"], d["w2"], d["w2_scale"], y.t, ws.t)
+        assert N.moe_status_read(ws.t) == N.MOE_OK
+        assert h.intact() and hs.intact() and y.intact() and ws.intact()
+        n = d["bounds"][-1]
+        want, off = ref.up(d["x"][:n], d["x_scale"][:n], d["bounds"], d["w13"], d["w13_scale"], act == "swiglu")
+        ref.check_quantized(h.t[:n], hs.t[:n], want, off, "h")
+        want, off = ref.down(h.t[:n], hs.t[:n], d["bounds"], d["w2"], d["w2_scale"])
+        over = (y.t[:n].to(D) - want).abs() - off
+        assert (over <= 0).all(), f"y: {int((over > 0).sum())} outside, worst by {over.max():.3e}"
+        assert torch.all(h.t[n:] == 0x5A) and torch.all(hs.t[n:] == 7.0) and torch.all(y.t[n:].view(U8) == 0x5A)
+
+
 def test_no_rows():
     d = problem([0, 0, 0], 128, 128, "swiglu", 1, extra=4)
     ws = N.workspace(d["shape"], dev())
