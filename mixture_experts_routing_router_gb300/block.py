@@ -3,10 +3,12 @@
     n = layernorm(x);  logits = n w_gate^T;  (ids, w) = softmax top-k of logits
     out = x + sum_j w_j * FFN_{ids_j}(n)
 
-Forward: moe_layernorm, moe_gate, moe_route, moe_dispatch, moe_expert_up_train,
+(or, with a ``router``, group-limited routing: its scores, groups and weights).
+
+Forward: moe_layernorm, moe_gate, moe_route (moe_route_grouped), moe_dispatch, moe_expert_up_train,
 moe_expert_down, moe_combine (the residual x added there).  Backward:
-moe_combine_backward, moe_route_backward, moe_expert_down_backward,
-moe_expert_up_backward, moe_gate_backward, moe_dispatch_backward (the gate's part
+moe_combine_backward, moe_route_backward (moe_route_grouped_backward),
+moe_expert_down_backward, moe_expert_up_backward, moe_gate_backward, moe_dispatch_backward (the gate's part
 of dn added there) and moe_layernorm_backward (the residual's gradient added
 there).  torch carries memory, streams and the autograd graph; every number comes
 from the library's kernels.  dn is rounded twice: the gate's part to BF16 (g w_gate), then
@@ -56,15 +58,19 @@ class _MoEBlockFn(torch.autograd.Function):
         N.moe_layernorm(x, gamma, beta, block.eps, n, mean, rstd)
         logits, ids, w = f32(T, E), i32(T, k), f32(T, k)
         N.moe_gate(shape, n, w_gate, logits, ws)
-        N.moe_route(shape, logits, ids, w, ws)
+        if block.router is None:
+            N.moe_route(shape, logits, ids, w, ws)
+        else:
+            N.moe_route_grouped(shape, block.router, logits, block.route_bias, ids, w, ws)
         offsets, dest, x_perm = i32(E + 1), i32(R), b16(R, H)
         N.moe_dispatch(shape, n, ids, i32(E), offsets, dest, i32(R), x_perm, ws)
         pre, h, y_perm, out = b16(R, up), b16(R, I), b16(R, H), torch.empty_like(x)
         N.moe_expert_up_train(shape, x_perm, offsets, w13, pre, h, ws)
         N.moe_expert_down(shape, h, offsets, w2, None, y_perm, None, ws)
         N.moe_combine(shape, y_perm, dest, w, None, out, ws, residual=x)
-        ctx.save_for_backward(x, gamma, w_gate, w13, w2, n, mean, rstd, ids, w, offsets, dest, x_perm, pre, h, y_perm)
-        ctx.block = block
+        ctx.save_for_backward(x, gamma, w_gate, w13, w2, n, mean, rstd, ids, w, offsets, dest, x_perm, pre, h, y_perm,
+                              logits if block.router is not None else None)
+        ctx.block, ctx.router = block, block.router
         return out
 
     @staticmethod
@@ -77,14 +83,18 @@ class _MoEBlockFn(torch.autograd.Function):
 
     @staticmethod
     def _gradients(ctx, dout):
-        x, gamma, w_gate, w13, w2, n, mean, rstd, ids, w, offsets, dest, x_perm, pre, h, y_perm = ctx.saved_tensors
+        (x, gamma, w_gate, w13, w2, n, mean, rstd, ids, w, offsets, dest, x_perm, pre, h, y_perm,
+         logits) = ctx.saved_tensors
         shape, ws = ctx.block._layer(x.shape[0], x.device)     # the block's, where check() looks
         want = ctx.needs_input_grad
         like = lambda t, on: torch.empty_like(t) if on else None
         dout = dout.contiguous()
         dy_perm, dw, dlogits = torch.empty_like(y_perm), torch.empty_like(w), w.new_empty(shape.tokens, shape.experts)
         N.moe_combine_backward(shape, dout, y_perm, dest, w, dy_perm, dw, ws)
-        N.moe_route_backward(shape, ids, w, dw, dlogits, ws)
+        if ctx.router is None:
+            N.moe_route_backward(shape, ids, w, dw, dlogits, ws)
+        else:
+            N.moe_route_grouped_backward(shape, ctx.router, logits, ids, dw, dlogits, ws)
         dpre, dx_perm = torch.empty_like(pre), torch.empty_like(x_perm)
         dw13, dw2, dw_gate = like(w13, want[4]), like(w2, want[5]), like(w_gate, want[3])
         N.moe_expert_down_backward(shape, dy_perm, offsets, w2, pre, h, dpre, dw2, ws)
@@ -111,10 +121,20 @@ class MoEBlock(torch.nn.Module):
     on one stream at a time.  Device-side errors (non-finite logits, a bounded wait that
     ran out), of any batch and either direction, stay there until ``check`` reads them.
     Differentiable once: a second
-    derivative through the block raises."""
+    derivative through the block raises.
 
-    def __init__(self, hidden, experts, top_k, inter, act=N.MOE_ACT_SWIGLU, eps=1e-5, device="cuda", generator=None):
+    ``router`` (native.make_router) has the tokens routed by moe_route_grouped; the block
+    then has a buffer ``route_bias`` [experts] FP32, zeros at first, that only selects: it
+    has no gradient, and a program that balances its experts adds to it between steps."""
+
+    def __init__(self, hidden, experts, top_k, inter, act=N.MOE_ACT_SWIGLU, eps=1e-5, device="cuda", generator=None,
+                 router=None):
         super().__init__()
+        if router is not None and not isinstance(router, N.moe_router):
+            raise ValueError(f"MoEBlock: router must come from native.make_router, got {type(router).__name__}")
+        self.router = router
+        if router is not None:
+            self.register_buffer("route_bias", torch.zeros(experts, device=device))
         up = 2 * inter if act == N.MOE_ACT_SWIGLU else inter
         self.hidden, self.experts, self.top_k, self.inter, self.act, self.eps = hidden, experts, top_k, inter, act, eps
 
@@ -154,6 +174,9 @@ class MoEBlock(torch.nn.Module):
             if w.dtype != torch.bfloat16 or w.shape != want:        # the kernels read them as they lie
                 raise ValueError(f"MoEBlock: {name} must be bfloat16 {want}, got {w.dtype} {tuple(w.shape)} "
                                  "(gamma and beta may be float32 or bfloat16)")
+        if self.router is not None and (self.route_bias.dtype != torch.float32 or self.route_bias.shape != (self.experts,)):
+            raise ValueError(f"MoEBlock: route_bias must be float32 ({self.experts},), got {self.route_bias.dtype} "
+                             f"{tuple(self.route_bias.shape)}")
         return _MoEBlockFn.apply(x.contiguous(), self.gamma, self.beta, self.w_gate, self.w13, self.w2, self)
 
     def check(self):

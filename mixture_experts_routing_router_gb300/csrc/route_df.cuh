@@ -19,6 +19,15 @@ namespace moe {
 
 struct Df { float h, l; };
 
+// A product rounded by itself: contracted into a sum it would no longer be the number whose
+// error the next line takes.
+MOE_DF float df_product(float a, float b) {
+#if defined(__CUDA_ARCH__)
+    return __fmul_rn(a, b);
+#else
+    return a * b;
+#endif
+}
 MOE_DF Df df_two_sum(float a, float b) {
     const float s = a + b, t = s - a;
     return {s, (a - (s - t)) + (b - t)};
@@ -34,13 +43,13 @@ MOE_DF Df df_add(Df a, Df b) {
     return df_fast_sum(s.h, s.l + t.l);
 }
 MOE_DF Df df_mul(Df a, Df b) {
-    const float p = a.h * b.h;
+    const float p = df_product(a.h, b.h);
     return df_fast_sum(p, fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, a.l * b.h));
 }
 MOE_DF Df df_div(Df a, Df b) {
     const float q1 = a.h / b.h;
     // a - q1 b, in which the leading parts cancel
-    const float p = q1 * b.h;
+    const float p = df_product(q1, b.h);
     const Df r = df_add(a, {-p, -fmaf(q1, b.l, fmaf(q1, b.h, -p))});
     const float q2 = r.h / b.h;
     const float q3 = (fmaf(-q2, b.h, r.h) + r.l - q2 * b.l) / b.h;
@@ -60,7 +69,7 @@ MOE_DF Df df_exp(Df x) {
     constexpr float kL1 = 0.693359375f;                               // 10 bits: n kL1 is exact
     constexpr Df kL2 = df_const(kLn2 - 0.693359375);
     const float n = rintf(x.h * 1.44269504f);
-    const float p = -n * kL2.h;
+    const float p = df_product(-n, kL2.h);
     Df r = df_add({fmaf(-n, kL1, x.h), x.l}, {p, fmaf(-n, kL2.h, -p) - n * kL2.l});
     float t = 1.0f / 479001600.0f;                                    // 1/12!
     t = fmaf(t, r.h, 1.0f / 39916800.0f);
