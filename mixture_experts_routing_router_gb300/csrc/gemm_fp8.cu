@@ -133,6 +133,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         tmem_alloc(smem_u32(&ctl->tmem_base), 512);
         tmem_relinquish();
     }
+    __syncthreads();                          // tensor memory is allocated before a dependent kernel may start
     pdl_wait();
     pdl_trigger();
     const int total = f_tile_list<F_THREADS, F_BM>(p, prefix, start, ctl->wtot);
@@ -393,6 +394,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 parity ^= 1;
             }
         }
+        cp_async_wait();                      // of a tile that was given up
     }
 
     tc_fence_before();
@@ -411,9 +413,7 @@ moe_status launch_f(const Fp8Problem& g, FParams p, const CUtensorMap& mw, const
     p.ntn = (g.N + BN - 1) / BN;
     const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + F_EPI_WARPS * F_STORE +
                         sizeof(FCtl) + (size_t)(3 * g.groups + 1) * sizeof(int);
-    // the attribute belongs to the device that is current: set with every launch
-    cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<MODE, NSUB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         F_MAX_SMEM);
+    cudaError_t e = allow_smem(fp8_gemm_kernel<MODE, NSUB>);
     if (e == cudaSuccess) {
         const long long used = g.rows < g.groups ? g.rows : g.groups;
         const long long tiles = (g.rows / F_BM + used) * p.ntn;     // at most

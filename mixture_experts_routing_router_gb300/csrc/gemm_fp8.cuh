@@ -166,6 +166,13 @@ __device__ __forceinline__ FTile f_tile(int tile, int& lo, const int* prefix, co
     return t;
 }
 
+// Lets a kernel have F_MAX_SMEM bytes of shared memory on the current device: the attribute
+// belongs to the device, so it is set there with every launch.
+template <typename... Args>
+inline cudaError_t allow_smem(void (*kernel)(Args...)) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F_MAX_SMEM);
+}
+
 // The tile list from the bucket bounds (clamped to the rows there are; empty after a
 // capacity overflow of the same layer call): `prefix` [groups + 1] tiles before a group,
 // `start` [groups] first rows and [groups] rows.  `wtot`: a word a warp.  All threads;

@@ -94,6 +94,7 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         tmem_alloc(smem_u32(&ctl->tmem_base), C::TMEM_COLS);
         tmem_relinquish();
     }
+    __syncthreads();                          // tensor memory is allocated before a dependent kernel may start
     if (!early) {
         pdl_wait();
         pdl_trigger();
@@ -374,6 +375,7 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 parity ^= 1;
             }
         }
+        cp_async_wait();                      // of a tile that was given up
     }
 
     tc_fence_before();
@@ -393,9 +395,7 @@ moe_status launch_r(const Fp8Problem& g, FParams p, const CUtensorMap& mw, cudaS
     CUtensorMap ma;
     if (!make_tensor_map_u8_rows(&ma, g.a, g.rows, g.K, g.K, 128u, (unsigned)NB)) return MOE_ERR_CUDA;
     const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + sizeof(RCtl) + (size_t)(3 * g.groups + 1) * sizeof(int);
-    // the attribute belongs to the device that is current: set with every launch
-    cudaError_t e = cudaFuncSetAttribute(fp8_rows_kernel<MODE, NSUB, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         F_MAX_SMEM);
+    cudaError_t e = allow_smem(fp8_rows_kernel<MODE, NSUB, NB>);
     if (e == cudaSuccess) {
         const long long used = g.rows < g.groups ? g.rows : g.groups;
         const long long tiles = (g.rows / NB + used) * p.ntn;         // at most

@@ -2,6 +2,7 @@
 return before any CUDA call), and the rules on their kernel's waits."""
 import ctypes
 import math
+import re
 
 import pytest
 import torch
@@ -179,14 +180,14 @@ def test_the_binding_refuses_tensors_that_do_not_fit(L, act, call, arg):
         go(4096)                                                  # a plain address: the C call refuses the workspace
 
 
-def test_waits_of_the_fp8_kernel():
+@pytest.mark.parametrize("name", ["gemm_fp8.cu", "gemm_fp8_rows.cu"])
+def test_waits_of_the_fp8_kernels(name):
     """The rules of the other GEMMs: a warp gives up a wait as a whole (a wait that is not the
     warp's stands in a block of one thread), and no barrier without a limit between roles."""
-    import re
-    (kernel, body), = W.kernels("gemm_fp8.cu")
+    (kernel, body), = W.kernels(name)
     alone = list(re.finditer(r"\b(mbar_wait_bounded|wait_armed_stages)\(", body))
     assert len(alone) == 2 and body.count("mbar_wait_warp(") == 5
     for m in alone:
         assert any(W.SINGLE.search(h) for h in W.enclosing(body, m.start())), body[m.start():m.start() + 70]
-    roles = body[body.index("if (warp < 4) {"):body.rindex("tc_fence_before")]
+    roles = body[body.index("if (warp == 0) {"):body.rindex("tc_fence_before")]
     assert "bar.sync" not in roles and "__syncthreads" not in roles

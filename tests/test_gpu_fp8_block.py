@@ -114,7 +114,7 @@ def test_dispatch_over_capacity_moves_nothing():
 BUCKETS = {
     "one": [1], "few": [0, 3, 0, 8, 9, 1], "edges": [32, 33, 96, 97, 127, 128, 129], "big": [300, 0, 513],
     "mixed": [1, 8, 129, 200, 256, 257, 700, 1000],
-    "many": [(7 * i) % 11 for i in range(300)],
+    "many": [(7 * i) % 11 for i in range(300)], "thousand": [(5 * i) % 4 for i in range(1024)],
 }
 WIDTHS = [(16, 16), (128, 128), (144, 112), (272, 400), (1024, 640), (2064, 144)]
 
@@ -142,7 +142,7 @@ def problem(buckets, H, I, act, seed, extra=3):
 @pytest.mark.parametrize("name", sorted(BUCKETS))
 def test_products(name, width, act):
     H, I = width
-    if name == "many" and H * I > 300000:
+    if name in ("many", "thousand") and H * I > 40000:
         pytest.skip("covered by the smaller widths")
     d = problem(BUCKETS[name], H, I, act, seed=H + I)
     ws = guarded_workspace(d["shape"])
@@ -251,6 +251,51 @@ def test_a_row_that_is_not_finite_stays_alone():
     assert torch.isnan(y[7].float()).all()
     keep = [r for r in range(45) if r != 7]
     assert torch.equal(y[keep].view(torch.int16), clean[keep].view(torch.int16))
+
+
+def test_few_rows_of_a_thousand_experts():
+    """64 tokens to 32 of 1024 experts: about two rows a group, the largest group lists."""
+    H, I, E, k, T = 144, 112, 1024, 32, 64
+    buckets = [2 if e % 5 else 1 for e in range(E)]
+    d = problem(buckets, H, I, "swiglu", seed=3, extra=T * k - sum(buckets))
+    shape = N.make_shape(T, H, E, k, I)
+    ws = N.workspace(shape, dev())
+    h, hs = torch.empty((T * k, I), dtype=U8, device=dev()), torch.empty((T * k, 1), device=dev())
+    y = torch.empty((T * k, H), dtype=BF16, device=dev())
+    N.moe_expert_up_fp8_block(shape, d["x"], d["x_scale"], d["offsets"], d["w13"], d["w13_scale"], h, hs, ws)
+    N.moe_expert_down_fp8_block(shape, h, hs, d["offsets"], d["w2"], d["w2_scale"], y, ws)
+    assert N.moe_status_read(ws) == N.MOE_OK
+    n = d["bounds"][-1]
+    ref.check_quantized(h[:n], hs[:n], *ref.up(d["x"][:n], d["x_scale"][:n], d["bounds"], d["w13"], d["w13_scale"], True), "h")
+    want, off = ref.down(h[:n], hs[:n], d["bounds"], d["w2"], d["w2_scale"])
+    assert ((y[:n].to(D) - want).abs() <= off).all()
+
+
+@pytest.mark.parametrize("rows", [5, 200])
+def test_nan_weights_reach_their_outputs_only(rows):
+    """A NaN code of w2 makes its column of its expert NaN; one of w13 the rows of its expert."""
+    d = problem([rows, rows], 272, 144, "swiglu", seed=2, extra=0)
+    shape, R = N.make_shape(2 * rows, 272, 2, 1, 144), 2 * rows
+
+    def run():
+        ws = N.workspace(shape, dev())
+        h, hs = torch.empty((R, 144), dtype=U8, device=dev()), torch.empty((R, 2), device=dev())
+        y = torch.empty((R, 272), dtype=BF16, device=dev())
+        N.moe_expert_up_fp8_block(shape, d["x"], d["x_scale"], d["offsets"], d["w13"], d["w13_scale"], h, hs, ws)
+        N.moe_expert_down_fp8_block(shape, h, hs, d["offsets"], d["w2"], d["w2_scale"], y, ws)
+        assert N.moe_status_read(ws) == N.MOE_OK
+        return y
+
+    clean = run()
+    keep = d["w2"][1, 130, 77].clone()
+    d["w2"][1, 130, 77] = 0x7F
+    y = run()
+    nan = torch.isnan(y)
+    assert nan[rows:, 130].all() and int(nan.sum()) == rows
+    assert torch.equal(y[~nan], clean[~nan])
+    d["w2"][1, 130, 77], d["w13"][0, 1, 7, 9] = keep, 0xFF
+    y = run()
+    assert torch.isnan(y[:rows]).all() and torch.equal(y[rows:].view(torch.int16), clean[rows:].view(torch.int16))
 
 
 def test_buckets_outside_the_rows_are_clamped():
