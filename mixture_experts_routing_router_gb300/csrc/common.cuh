@@ -5,6 +5,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cstring>
 #include <utility>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -116,7 +117,7 @@ struct WsLayout {
     int count_tiles;
 };
 
-inline WsLayout ws_layout(const moe_shape& s) {
+inline WsLayout ws_layout_of(const moe_shape& s) {
     WsLayout L{};
     const size_t T = (size_t)s.tokens, H = (size_t)s.hidden, E = (size_t)s.experts;
     const size_t R = T * (size_t)s.top_k, I = (size_t)s.inter;
@@ -141,6 +142,18 @@ inline WsLayout ws_layout(const moe_shape& s) {
     L.sync = o;         o = align_up(o + (E + 4 * ((H + 127) / 128) + 1) * 4, kAlign);
     L.total = o;
     return L;
+}
+
+// The layout of the shape that this host thread asked about last is kept: a call asks for it
+// one to three times, and working it out (the gradients' split plans) takes 0.7 us.
+inline const WsLayout& ws_layout(const moe_shape& s) {
+    thread_local moe_shape shape{};
+    thread_local WsLayout layout{};
+    if (std::memcmp(&shape, &s, sizeof(s)) != 0) {
+        layout = ws_layout_of(s);
+        shape = s;
+    }
+    return layout;
 }
 
 // Bounded waits give up after this long and raise MOE_ERR_TIMEOUT.
