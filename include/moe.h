@@ -363,7 +363,8 @@ MOE_API moe_status moe_layer_nvfp4(const moe_shape* shape, const float* logits, 
 /* moe_dispatch with the rows quantized on the way:
  *   x       device bf16 [T, H]
  *   x_perm  device u8 [T*k, H], x_scale device f32 [T*k, nb(H)]  out: row dest[p] is x[p / k]
- * The other arguments, the placement and the device errors are those of moe_dispatch. */
+ * The other arguments, the placement and the device errors are those of moe_dispatch.
+ * Up to 12288 pairs run without the look-back (moe_workspace_set_wait has no effect). */
 MOE_API moe_status moe_dispatch_fp8_block(const moe_shape* shape, const uint16_t* x, const int32_t* topk_ids,
                                           int32_t* counts, int32_t* offsets, int32_t* dest, int32_t* sorted_pair,
                                           uint8_t* x_perm, float* x_scale, void* ws, size_t ws_bytes, void* stream);

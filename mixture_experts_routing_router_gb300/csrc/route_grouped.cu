@@ -12,14 +12,15 @@
 //   w_j   = scale * s_j, divided by the sum over the selection when `renorm`.
 //
 // Keys are defined through double so that every implementation selects the same
-// experts, but the double unit is slow here (two results a cycle and SM; a token's scores
-// in double take a warp 10 us, in pairs of floats, route_df.cuh, about one).  The kernel
-// therefore works on FP32 keys with a bound on their error (`eps`, below) and checks
+// experts, but the double unit is slow here (two results a cycle and SM).  The kernel
+// therefore works on FP32 keys with a bound on their error (key_margin) and checks
 // that every comparison the result hangs on -- chosen against other groups, each
 // selected key against the next one -- is decided by more than that; a token where one
 // is not (about one in a thousand with random logits) is selected again from the
 // defined keys: the winners next to one another among themselves, all experts where the
-// groups are in doubt.  Two experts of equal logit and bias have equal keys either way.
+// groups are in doubt.  That adds 2 us to a call with sigmoid scores, 4 with softmax scores
+// and 6 for all experts; in double, without the pairs of floats of route_df.cuh, 10.  Two
+// experts of equal logit and bias have equal keys either way.
 #include "common.cuh"
 #include "route_df.cuh"
 #include "route_warp.cuh"
@@ -140,7 +141,7 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
 }
 
 // EPL = experts per lane (E <= 32 * EPL; FULL: equal); lane l holds experts l, l + 32, ...
-// Bound by instructions (16384 tokens of 256 experts, 8 groups: NOW_LARGE us; selects
+// Bound by instructions (16384 tokens of 256 experts, 8 groups: 27 us; selects
 // instead of branches, and what a warp's tokens share kept in registers -- biases, a
 // key's place in shared memory and its group -- took it from 1500 to about 700 a token).
 // A lane keeps its two best candidates, so that most rounds of warp-wide argmax need no
@@ -368,7 +369,7 @@ route_grouped_kernel(int T, int E, int k, const moe_router r, const float* __res
 // or above k): 32 / G tokens a warp zero their rows together, then lane j of a token writes
 // its j-th expert's gradient.  An id out of range or repeated inside the token (the first
 // stays valid, as in the dispatch) takes no part and raises the status.
-// Bound by writing the rows (16384 x 256, k = 8: BWD_LARGE us; a warp a token: 9.4).
+// Bound by writing the rows (16384 x 256, k = 8: 5.5 us, 17 MB; a warp a token: 9.4).
 template <int G>
 __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll

@@ -214,6 +214,42 @@ def make_fp8_weights(wl: Workload, seed: int = 0, device="cpu", unit_scale: bool
     return d
 
 
+def quantize_blocks_fp8(w: torch.Tensor):
+    """Input preparation for block-scaled FP8 expert weights: each block of 128 x 128
+    of ``w`` [..., rows, K] (cut off at the edges) becomes E4M3 codes (torch's
+    round-to-nearest float8_e4m3fn conversion) of w / scale with
+    scale = max|block| / 448 (1 for an all-zero block).
+    -> (codes uint8 [..., rows, K], scale float32 [..., ceil(rows/128), ceil(K/128)])."""
+    rows, K = w.shape[-2:]
+    nr, nk = (rows + 127) // 128, (K + 127) // 128
+    wf = torch.nn.functional.pad(w.float(), (0, nk * 128 - K, 0, nr * 128 - rows))
+    blk = wf.unflatten(-1, (nk, 128)).unflatten(-3, (nr, 128))       # [..., nr, 128, nk, 128]
+    amax = blk.abs().amax(dim=(-3, -1))
+    scale = torch.where(amax > 0, amax / 448.0, torch.ones_like(amax))
+    codes = (blk / scale[..., :, None, :, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    codes = codes.flatten(-2).flatten(-3, -2)[..., :rows, :K]
+    return codes.contiguous(), scale.contiguous()
+
+
+def make_fp8_block_weights(wl: Workload, seed: int = 0, device="cpu", unit_scale: bool = False) -> dict:
+    """Block-scaled FP8 expert weights quantized from the same per-expert BF16 draws as
+    make_inputs, P = up / I matrices an expert with blocks of their own:
+    w13 uint8 [E, up, H], s13 float32 [E, P, ceil(I/128), ceil(H/128)],
+    w2 uint8 [E, H, I], s2 float32 [E, ceil(H/128), ceil(I/128)]."""
+    E, H, I = wl.experts, wl.hidden, wl.inter
+    P, nb = wl.up // I, lambda n: (n + 127) // 128
+    d = {"w13": torch.empty((E, wl.up, H), dtype=torch.uint8, device=device),
+         "s13": torch.empty((E, P, nb(I), nb(H)), dtype=torch.float32, device=device),
+         "w2": torch.empty((E, H, I), dtype=torch.uint8, device=device),
+         "s2": torch.empty((E, nb(H), nb(I)), dtype=torch.float32, device=device)}
+    for e in range(E):
+        a, b = expert_weights(wl, e, seed, device, unit_scale)
+        codes, d["s13"][e] = quantize_blocks_fp8(a.view(P, I, H))
+        d["w13"][e] = codes.view(wl.up, H)
+        d["w2"][e], d["s2"][e] = quantize_blocks_fp8(b)
+    return d
+
+
 E2M1_MAGNITUDES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 
 
