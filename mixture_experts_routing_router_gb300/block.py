@@ -58,10 +58,11 @@ class _MoEBlockFn(torch.autograd.Function):
         N.moe_layernorm(x, gamma, beta, block.eps, n, mean, rstd)
         logits, ids, w = f32(T, E), i32(T, k), f32(T, k)
         N.moe_gate(shape, n, w_gate, logits, ws)
-        if block.router is None:
+        router = block.router and N.moe_router.from_buffer_copy(block.router)  # as it is now, for the backward pass too
+        if router is None:
             N.moe_route(shape, logits, ids, w, ws)
         else:
-            N.moe_route_grouped(shape, block.router, logits, block.route_bias, ids, w, ws)
+            N.moe_route_grouped(shape, router, logits, block.route_bias, ids, w, ws)
         offsets, dest, x_perm = i32(E + 1), i32(R), b16(R, H)
         N.moe_dispatch(shape, n, ids, i32(E), offsets, dest, i32(R), x_perm, ws)
         pre, h, y_perm, out = b16(R, up), b16(R, I), b16(R, H), torch.empty_like(x)
@@ -69,8 +70,8 @@ class _MoEBlockFn(torch.autograd.Function):
         N.moe_expert_down(shape, h, offsets, w2, None, y_perm, None, ws)
         N.moe_combine(shape, y_perm, dest, w, None, out, ws, residual=x)
         ctx.save_for_backward(x, gamma, w_gate, w13, w2, n, mean, rstd, ids, w, offsets, dest, x_perm, pre, h, y_perm,
-                              logits if block.router is not None else None)
-        ctx.block, ctx.router = block, block.router
+                              logits if router is not None else None)
+        ctx.block, ctx.router = block, router
         return out
 
     @staticmethod

@@ -89,3 +89,16 @@ def test_other_routers_and_biases_are_refused():
     block.route_bias = block.route_bias.half()
     with pytest.raises(ValueError, match="route_bias"):
         block(x)
+
+
+def test_the_backward_pass_uses_the_router_of_its_forward():
+    gen = torch.Generator(device=dev()).manual_seed(2)
+    block = MoEBlock(64, 16, 2, 64, device=dev(), generator=gen, router=N.make_router(groups=4, topk_groups=2, scale=2.0))
+    x = torch.randn(40, 64, generator=gen, device=dev()).to(torch.bfloat16)
+    grads = []
+    for scale in (2.0, 8.0):
+        block.router.scale = 2.0
+        loss = block(x).float().square().sum()
+        block.router.scale = scale                       # for the next batch
+        grads.append(torch.autograd.grad(loss, [p for p in block.parameters()]))
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
