@@ -304,6 +304,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     break;
                 }
                 tc_fence_after();
+                // the MMAs get the accumulator back when it is read: for the plain product ahead of the
+                // last multiply-adds (2 % less time), for the activations' larger kernels after them
+                // (2 % less than ahead)
+                auto release = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[acc]));
+                };
+                constexpr bool kAhead = MODE == kGemmPlain;
                 if (any) {
                     const uint32_t ta = tmem + (uint32_t)(acc * C::ACC_COLS + 64 * hf) + ((uint32_t)(32 * q) << 16);
 #pragma unroll
@@ -312,15 +321,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         tmem_ld_cols(ta + (uint32_t)(s * 128), v);
                         tmem_ld_wait();
                         tmem_ld_done(v);
+                        if (kAhead && s == NSUB - 1) release();
                         const unsigned long long ff = pack_f32x2(f[s], f[s]);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             sum[s][i] = fma_f32x2(pack_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ff, sum[s][i]);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[acc]));
+                if (!kAhead || !any) release();
                 if (++acc == C::ACCS) { acc = 0; aph ^= 1u; }
             }
             if (!ok) break;
