@@ -67,7 +67,7 @@ moe_status do_dispatch(const moe_shape& s, const uint16_t* x, const int32_t* ids
 
 moe_status do_up(const moe_shape& s, const uint8_t* x_perm, const float* x_scale, const int32_t* offsets,
                  const uint8_t* w13, const float* w13_scale, uint8_t* h, float* h_scale, void* ws, cudaStream_t st,
-                 int gated) {
+                 int gated, const int32_t* ids) {
     Fp8Problem g{};
     g.mode = s.act == MOE_ACT_SWIGLU ? kGemmSwiGLU : kGemmReLU2;
     g.a = x_perm; g.a_scale = x_scale; g.rows = (long long)s.tokens * s.top_k;
@@ -77,6 +77,8 @@ moe_status do_up(const moe_shape& s, const uint8_t* x_perm, const float* x_scale
     g.out = h; g.out_scale = h_scale;
     g.max_group_rows = s.tokens;                   // a token's experts are distinct
     g.gated = gated;
+    g.early = ids != nullptr;                      // (the dispatch in front has waited for them)
+    g.ids = ids; g.top_k = s.top_k;
     return launch_fp8_gemm(g, at<WsHeader>(ws, 0), st);
 }
 
@@ -148,7 +150,8 @@ moe_status moe_expert_up_fp8_block(const moe_shape* shape, const uint8_t* x_perm
     if (!aligned(x_perm, 16) || !aligned(x_scale, 16) || !aligned(offsets, 16) || !aligned(w13, 16) ||
         !aligned(w13_scale, 16) || !aligned(h, 16) || !aligned(h_scale, 16))
         return MOE_ERR_INVALID_ARG;
-    return do_up(*shape, x_perm, x_scale, offsets, w13, w13_scale, h, h_scale, ws, static_cast<cudaStream_t>(stream), 0);
+    return do_up(*shape, x_perm, x_scale, offsets, w13, w13_scale, h, h_scale, ws, static_cast<cudaStream_t>(stream), 0,
+                 nullptr);
 }
 
 moe_status moe_expert_down_fp8_block(const moe_shape* shape, const uint8_t* h, const float* h_scale,
@@ -200,7 +203,8 @@ moe_status moe_layer_fp8_block(const moe_shape* shape, const float* logits, cons
     if ((r = do_dispatch(s, x, ids, at<int32_t>(ws, L.counts), offsets, dest, at<int32_t>(ws, L.sorted_pair), x_perm,
                          x_scale, ws, st)) != MOE_OK)
         return r;
-    if ((r = do_up(s, x_perm, x_scale, offsets, w13, w13_scale, h, h_scale, ws, st, 1)) != MOE_OK) return r;
+    if ((r = do_up(s, x_perm, x_scale, offsets, w13, w13_scale, h, h_scale, ws, st, 1, ids)) != MOE_OK)
+        return r;
     if ((r = do_down(s, h, h_scale, offsets, w2, w2_scale, y_perm, ws, st, 1, 1)) != MOE_OK) return r;
     return from_cuda(launch_combine(s, y_perm, dest, w, nullptr, residual, out, hdr, st));
 }

@@ -15,18 +15,22 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-// Four 128-column blocks, b0 .. b0 + 3, of a row (`src`, H columns) on one warp, 16 columns
-// a lane, to the slots dsh[0 .. k-1] (negative ones are left out).
-__device__ __forceinline__ void quantize_four_blocks(const uint16_t* src, int H, int nb, int b0, int lane, int k,
-                                                     const int* dsh, uint8_t* x_perm, float* x_scale) {
+// Four 128-column blocks, b0 .. b0 + 3, of a row (H columns) on one warp, 16 columns a lane.
+__device__ __forceinline__ void load_four_blocks(const uint16_t* src, int H, int b0, int lane, uint32_t (&u)[8]) {
     const int c = b0 * 128 + lane * 16;            // this lane's columns
-    const bool in = c < H;
-    uint32_t u[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    if (in) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src + c)), w = __ldcs(reinterpret_cast<const uint4*>(src + c) + 1);
-        u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
-        u[4] = w.x; u[5] = w.y; u[6] = w.z; u[7] = w.w;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u), w = v;
+    if (c < H) {
+        v = __ldcs(reinterpret_cast<const uint4*>(src + c));
+        w = __ldcs(reinterpret_cast<const uint4*>(src + c) + 1);
     }
+    u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+    u[4] = w.x; u[5] = w.y; u[6] = w.z; u[7] = w.w;
+}
+// Their codes and scales to the slots dsh[0 .. k-1] (negative ones are left out).
+__device__ __forceinline__ void quantize_four_blocks(const uint32_t (&u)[8], int H, int nb, int b0, int lane, int k,
+                                                     const int* dsh, uint8_t* x_perm, float* x_scale) {
+    const int c = b0 * 128 + lane * 16;
+    const bool in = c < H;
     float f[16], m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -78,8 +82,11 @@ scatter_fp8_kernel(int T, int H, int k, int E, const uint16_t* __restrict__ x, c
             dsh[tid] = d;
         }
         __syncthreads();
-        for (int b0 = 4 * warp; b0 < nb; b0 += 4 * warps)
-            quantize_four_blocks(x + (size_t)t * H, H, nb, b0, lane, k, dsh, x_perm, x_scale);
+        for (int b0 = 4 * warp; b0 < nb; b0 += 4 * warps) {
+            uint32_t u[8];
+            load_four_blocks(x + (size_t)t * H, H, b0, lane, u);
+            quantize_four_blocks(u, H, nb, b0, lane, k, dsh, x_perm, x_scale);
+        }
         __syncthreads();
     }
 }
@@ -107,6 +114,10 @@ dispatch_fp8_kernel(int T, int H, int k, int E, int capacity, const uint16_t* __
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t0 = (int)((long long)T * blockIdx.x / gridDim.x), t1 = (int)((long long)T * (blockIdx.x + 1) / gridDim.x);
     const bool lead = blockIdx.x == 0;
+    // the warp's first piece of a row is on its way while the pairs are counted
+    const int nb = (H + kFp8Block - 1) / kFp8Block, items = (nb + 3) / 4;
+    uint32_t u[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    if (warp < (t1 - t0) * items) load_four_blocks(x + (size_t)(t0 + warp / items) * H, H, 4 * (warp % items), lane, u);
     for (int e = tid; e < 2 * E; e += kSmallThreads) sm[e] = 0;
     __syncthreads();
     // whole tokens a warp: lanes of a token sit together, the first of equal ids counts
@@ -115,14 +126,14 @@ dispatch_fp8_kernel(int T, int H, int k, int E, int capacity, const uint16_t* __
     for (int tb = warp * tpw; tb < T; tb += kAhead * step) {
         int next[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int t = tb + u * step + lane / k;
-            next[u] = lane < used && t < T ? __ldg(ids + (size_t)(tb + u * step) * k + lane) : -1;
+        for (int a = 0; a < kAhead; ++a) {
+            const int t = tb + a * step + lane / k;
+            next[a] = lane < used && t < T ? __ldg(ids + (size_t)(tb + a * step) * k + lane) : -1;
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (tb + u * step >= T) break;
-            const int t = tb + u * step + lane / k, id = next[u];
+        for (int a = 0; a < kAhead; ++a) {
+            if (tb + a * step >= T) break;
+            const int t = tb + a * step + lane / k, id = next[a];
             const bool pair = lane < used && t < T;
             bool ok = pair && id >= 0 && id < E;
             for (int b = 1; b < k; ++b) {          // (a match over the warp took 60 cycles of the SM)
@@ -155,8 +166,7 @@ dispatch_fp8_kernel(int T, int H, int k, int E, int capacity, const uint16_t* __
     }
     if (lane == 31) wsum[warp] = inc;
     over = __syncthreads_or(over);
-    int run = inc - loc;
-    for (int w = 0; w < warp; ++w) run += wsum[w];
+    int run = inc - loc + __reduce_add_sync(kAll, lane < warp ? wsum[lane] : 0);
     for (int e = e0; e < min(e0 + per, E); ++e) {
         const int c = total[e];
         total[e] = run;
@@ -186,10 +196,10 @@ dispatch_fp8_kernel(int T, int H, int k, int E, int capacity, const uint16_t* __
     if (tid < own) mine[tid] = slot;
     __syncthreads();
     // ---- rows
-    const int nb = (H + kFp8Block - 1) / kFp8Block, items = (nb + 3) / 4;
     for (int i = warp; i < (t1 - t0) * items; i += kSmallThreads / 32) {
         const int t = i / items, b0 = 4 * (i - t * items);
-        quantize_four_blocks(x + (size_t)(t0 + t) * H, H, nb, b0, lane, k, mine + t * k, x_perm, x_scale);
+        if (i > warp) load_four_blocks(x + (size_t)(t0 + t) * H, H, b0, lane, u);
+        quantize_four_blocks(u, H, nb, b0, lane, k, mine + t * k, x_perm, x_scale);
     }
 }
 

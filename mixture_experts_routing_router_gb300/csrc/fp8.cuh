@@ -66,7 +66,8 @@ struct Fp8Problem {
     void* out; float* out_scale;               // plain: bf16 [rows, N]; else E4M3 [rows, N], [rows, ceil(N / 128)]
     int max_group_rows;                        // host bound on the rows of a group
     int gated;                                 // as GemmProblem
-    int early;                                 // 1: the bucket bounds are final when the kernel starts
+    int early;                                 // 1: the bucket bounds are final when the kernel starts, or
+    const int32_t* ids; int top_k;             //    (not null) the experts of every token, [rows / top_k, top_k]
 };
 moe_status launch_fp8_gemm(const Fp8Problem& p, WsHeader* hdr, cudaStream_t st);
 

@@ -132,6 +132,8 @@ struct FParams {
     float* out_scale;
     WsHeader* hdr;
     int gated;
+    const int32_t* ids;                         // few-row kernel: null, or what the bounds are counted from
+    int top_k;
 };
 
 struct FTile { int g, nt, row0, rows; };        // first row of the tile and how many it holds
@@ -199,8 +201,7 @@ __device__ __forceinline__ int f_tile_list(const FParams& p, int* prefix, int* s
     }
     if (lane == 31) wtot[warp] = inc;
     __syncthreads();
-    int run = inc - sum;
-    for (int w = 0; w < warp; ++w) run += wtot[w];
+    int run = inc - sum + __reduce_add_sync(0xffffffffu, lane < warp ? wtot[lane] : 0);
     for (int g = g0; g < min(g0 + per, p.groups); ++g) {
         prefix[g] = run;
         run += ((start[p.groups + g] + BM - 1) / BM) * p.ntn;

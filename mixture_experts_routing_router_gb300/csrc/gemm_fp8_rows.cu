@@ -21,9 +21,11 @@
 // output block is a warp-wide maximum of its bits, then one over the four warps of the same
 // rows through shared memory and an mbarrier.  Every wait is bounded.
 //
-// `early` (moe_layer_fp8_block's down projection): the bucket bounds were final before the
-// kernel in front of this one could start, so the tile list is built and the first stages'
-// weights are sent for before the programmatic wait.
+// `early` (inside moe_layer_fp8_block): what the tile list is built from was final before the
+// kernel in front of this one could start, so the list is built and the first stages' weights
+// are sent for before the programmatic wait.  For the down projection that is the bucket
+// bounds; for the up projection of at most R_THREADS pairs the tokens' experts, from which
+// every block counts the bounds itself, while the dispatch runs.
 #include "gemm_fp8.cuh"
 
 namespace moe {
@@ -57,9 +59,49 @@ struct RCtl {
     uint32_t tmem_base;
     int abort;
     int wtot[R_THREADS / 32];
+    int ids[R_THREADS];
     RScales scales[R_EPI_WARPS][2];
     alignas(16) uint32_t amax[2][2][64][4];     // [exchange parity][block][row][lane quarter] bits
 };
+
+// f_tile_list with the bounds counted from p.ids, a pair a thread: as the dispatch has them
+// (ids out of range, and those repeated in a token, are in no bucket).  Over capacity, where
+// the dispatch moves nothing, the rows are what the workspace holds, and no later kernel of
+// the call reads the results.
+template <int BM>
+__device__ __forceinline__ int r_tile_list(const FParams& p, int* prefix, int* start, int* ids, int* wtot) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int* count = start + p.groups;
+    for (int g = tid; g < p.groups; g += R_THREADS) count[g] = 0;
+    const int id = tid < p.rows ? __ldcg(p.ids + tid) : -1;
+    ids[tid] = id;
+    __syncthreads();
+    bool ok = id >= 0 && id < p.groups;
+    for (int j = tid - tid % p.top_k; ok && j < tid; ++j) ok = ids[j] != id;
+    if (ok) atomicAdd(&count[id], 1);
+    __syncthreads();
+    const int per = (p.groups + R_THREADS - 1) / R_THREADS, g0 = tid * per;
+    unsigned sum = 0;                            // rows, and tiles of 2^16 on
+    auto both = [&](int n) { return (unsigned)n | (unsigned)((n + BM - 1) / BM) << 16; };
+    for (int g = g0; g < min(g0 + per, p.groups); ++g) sum += both(count[g]);
+    unsigned inc = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const unsigned v = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += v;
+    }
+    if (lane == 31) wtot[warp] = (int)inc;
+    __syncthreads();
+    unsigned run = inc - sum + __reduce_add_sync(0xffffffffu, lane < warp ? (unsigned)wtot[lane] : 0u);
+    for (int g = g0; g < min(g0 + per, p.groups); ++g) {
+        start[g] = (int)(run & 0xffffu);
+        prefix[g] = (int)(run >> 16) * p.ntn;
+        run += both(count[g]);
+    }
+    if (tid == R_THREADS - 1) prefix[p.groups] = (int)(run >> 16) * p.ntn;
+    __syncthreads();
+    return prefix[p.groups];
+}
 
 template <int MODE, int NSUB, int NB>
 __global__ void __launch_bounds__(R_THREADS, 1)
@@ -105,7 +147,8 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         pdl_wait();
         pdl_trigger();
     }
-    const int total = f_tile_list<R_THREADS, NB>(p, prefix, start, ctl->wtot);
+    const int total = p.ids ? r_tile_list<NB>(p, prefix, start, ctl->ids, ctl->wtot)
+                            : f_tile_list<R_THREADS, NB>(p, prefix, start, ctl->wtot);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -398,6 +441,9 @@ moe_status launch_r(const Fp8Problem& g, FParams p, const CUtensorMap& mw, cudaS
     using C = RCfg<NSUB, NB>;
     constexpr int BN = MODE == kGemmSwiGLU ? 128 : 128 * NSUB;
     p.ntn = (g.N + BN - 1) / BN;
+    const bool counts = g.early && g.ids && g.rows <= R_THREADS;
+    p.ids = counts ? g.ids : nullptr;
+    p.top_k = g.top_k;
     CUtensorMap ma;
     if (!make_tensor_map_u8_rows(&ma, g.a, g.rows, g.K, g.K, 128u, (unsigned)NB)) return MOE_ERR_CUDA;
     const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + sizeof(RCtl) + (size_t)(3 * g.groups + 1) * sizeof(int);
@@ -407,7 +453,7 @@ moe_status launch_r(const Fp8Problem& g, FParams p, const CUtensorMap& mw, cudaS
         const long long tiles = (g.rows / NB + used) * p.ntn;         // at most
         const int sms = device_sm_count();
         e = launch_kernel(fp8_rows_kernel<MODE, NSUB, NB>, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(R_THREADS), smem,
-                          st, 1, kUsePdl, ma, mw, p, g.early);
+                          st, 1, kUsePdl, ma, mw, p, (int)(g.early && (counts || !g.ids)));
     }
     if (e == cudaSuccess) return MOE_OK;
     set_error("FP8 small-row GEMM launch (smem %zu): %s", smem, cudaGetErrorString(e));
