@@ -134,6 +134,7 @@ struct FParams {
     int gated;
     const int32_t* ids;                         // few-row kernel: null, or what the bounds are counted from
     int top_k;
+    int stages;                                 // few-row kernel: of its ring
 };
 
 struct FTile { int g, nt, row0, rows; };        // first row of the tile and how many it holds

@@ -35,11 +35,13 @@ constexpr int R_THREADS = 320;
 constexpr int R_EPI_WARPS = 8;
 constexpr int R_MAX_STAGES = 10;
 constexpr int R_MAX_ACCS = 8;
+constexpr size_t R_HALF_SMEM = 112 * 1024;      // two blocks an SM
 
 template <int NSUB, int NB>
 struct RCfg {
     static constexpr int STAGE_BYTES = NSUB * F_BOX + NB * 128;
     static constexpr int STAGES = 192 * 1024 / STAGE_BYTES < R_MAX_STAGES ? 192 * 1024 / STAGE_BYTES : R_MAX_STAGES;
+    static constexpr bool PAIR = NSUB == 1 && NB == 16;               // at most 102 registers, and short stages
     static constexpr int ACC_COLS = NSUB * NB;
     static constexpr int ACCS = 512 / ACC_COLS < R_MAX_ACCS ? 512 / ACC_COLS : R_MAX_ACCS;
     static constexpr uint32_t TMEM_COLS = ACCS * ACC_COLS;            // a power of two
@@ -111,17 +113,18 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     constexpr bool UP = MODE != kGemmPlain;
     constexpr int BN = MODE == kGemmSwiGLU ? 128 : 128 * NSUB;        // output columns of a tile
     constexpr int HB = NB / 2;                                        // rows of a thread
+    const int stages = p.stages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
-    RCtl* ctl = reinterpret_cast<RCtl*>(smem + C::STAGES * C::STAGE_BYTES);
+    RCtl* ctl = reinterpret_cast<RCtl*>(smem + stages * C::STAGE_BYTES);
     int* prefix = reinterpret_cast<int*>(ctl + 1);                    // [groups + 1]
     int* start = prefix + p.groups + 1;                               // [groups] first row, [groups] rows
     const uint32_t smem_base = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(smem_u32(&ctl->full[s]), 1);
             mbar_init(smem_u32(&ctl->empty[s]), 1);
         }
@@ -169,7 +172,7 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         if (tid == 0 && (int)blockIdx.x < total) {
             int group = 0;
             const FTile t = f_tile<UP, NB>(blockIdx.x, group, prefix, start, p);
-            for (; ahead < min(C::STAGES, p.nkb); ++ahead) load_weights(t, ahead, ahead);
+            for (; ahead < min(stages, p.nkb); ++ahead) load_weights(t, ahead, ahead);
         }
         pdl_wait();
         pdl_trigger();
@@ -192,13 +195,13 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     tma_load_2d(smem_base + (uint32_t)(stage * C::STAGE_BYTES + NSUB * F_BOX), &tmA,
                                 smem_u32(&ctl->full[stage]), kb * 128, t.row0);
                     ++armed;
-                    if (++stage == C::STAGES) { stage = 0; ph ^= 1u; }
+                    if (++stage == stages) { stage = 0; ph ^= 1u; }
                 }
             }
             if (!ok) {
                 // (stages armed before the wait whose rows never went out cannot complete: their
                 // wait runs out and the fixed delay follows)
-                if (!wait_armed_stages(smem_u32(&ctl->full[0]), C::STAGES, max(armed, (long long)ahead))) settle_delay();
+                if (!wait_armed_stages(smem_u32(&ctl->full[0]), stages, max(armed, (long long)ahead))) settle_delay();
                 raise_status(p.hdr, MOE_ERR_TIMEOUT);
                 p.hdr->timeout_site = kSiteGemmProducer;
             }
@@ -231,7 +234,7 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     tc_commit(smem_u32(&ctl->empty[stage]));
                 }
                 __syncwarp();
-                if (++stage == C::STAGES) { stage = 0; ph ^= 1u; }
+                if (++stage == stages) { stage = 0; ph ^= 1u; }
                 if (++acc == C::ACCS) { acc = 0; aph ^= 1u; }
             }
         }
@@ -446,15 +449,19 @@ moe_status launch_r(const Fp8Problem& g, FParams p, const CUtensorMap& mw, cudaS
     p.top_k = g.top_k;
     CUtensorMap ma;
     if (!make_tensor_map_u8_rows(&ma, g.a, g.rows, g.K, g.K, 128u, (unsigned)NB)) return MOE_ERR_CUDA;
-    const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + sizeof(RCtl) + (size_t)(3 * g.groups + 1) * sizeof(int);
+    const size_t rest = 1024 + sizeof(RCtl) + (size_t)(3 * g.groups + 1) * sizeof(int);
+    const long long used = g.rows < g.groups ? g.rows : g.groups;
+    const long long tiles = (g.rows / NB + used) * p.ntn;             // at most
+    const int sms = device_sm_count();
+    // With a tile an SM at most, a ring that leaves room for a block of the next kernel of the
+    // layer, which then starts its weights in time (1 token, 9 experts: a layer 24.3 -> 23.1 us).
+    p.stages = C::STAGES;
+    if (C::PAIR && tiles <= sms) p.stages = (int)((R_HALF_SMEM - rest) / C::STAGE_BYTES);
+    const size_t smem = rest + (size_t)p.stages * C::STAGE_BYTES;
     cudaError_t e = allow_smem(fp8_rows_kernel<MODE, NSUB, NB>);
-    if (e == cudaSuccess) {
-        const long long used = g.rows < g.groups ? g.rows : g.groups;
-        const long long tiles = (g.rows / NB + used) * p.ntn;         // at most
-        const int sms = device_sm_count();
+    if (e == cudaSuccess)
         e = launch_kernel(fp8_rows_kernel<MODE, NSUB, NB>, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(R_THREADS), smem,
                           st, 1, kUsePdl, ma, mw, p, (int)(g.early && (counts || !g.ids)));
-    }
     if (e == cudaSuccess) return MOE_OK;
     set_error("FP8 small-row GEMM launch (smem %zu): %s", smem, cudaGetErrorString(e));
     return MOE_ERR_CUDA;
