@@ -77,6 +77,43 @@ def test_dispatch(size, bad):
     assert torch.all(out[4].t[n:] == 0x5A)                       # rows behind the last one
 
 
+@pytest.mark.parametrize("size", [(20000, 16, 300, 3), (4099, 32, 1024, 32), (70001, 16, 33, 1), (5003, 16, 7, 7)], ids=str)
+def test_dispatch_of_many_tiles(size):
+    """More tiles of pairs than a scan has warps, tokens across the edges of warps and tiles,
+    repeated and invalid ids everywhere, then a call over capacity and a valid one again, and the
+    unquantized dispatch between them on the same workspace."""
+    T, H, E, k = size
+    g = torch.Generator().manual_seed(E)
+    ids = torch.randint(-1, E + 1, (T, k), generator=g, dtype=I32)
+    ids[T // 3:T // 2] = torch.arange(k, dtype=I32)[None] % E
+    ids = ids.to(dev())
+    x = rows_of(gen(4), T, H)
+    shape = N.make_shape(T, H, E, k, 16)
+    ws = guarded_workspace(shape)
+    i32 = lambda *s: torch.empty(s, dtype=I32, device=dev())
+    plain = [i32(E), i32(E + 1), i32(T * k), i32(T * k), torch.empty((T * k, H), dtype=BF16, device=dev())]
+    for _ in range(2):
+        out = dispatch_buffers(T, H, E, k)
+        out[4].t.fill_(0x5A)
+        N.moe_dispatch_fp8_block(shape, x, ids, *(o.t for o in out), ws.t)
+        assert N.moe_status_read(ws.t) == N.MOE_ERR_INVALID_ROUTE
+        assert all(o.intact() for o in out) and ws.intact()
+        N.moe_dispatch(shape, x, ids, *plain, ws.t)
+        assert N.moe_status_read(ws.t) == N.MOE_ERR_INVALID_ROUTE
+        n = int(plain[1][-1])
+        assert all(torch.equal(a.t, b) for a, b in zip(out[:3], plain[:3]))
+        assert torch.equal(out[3].t[:n], plain[3][:n])
+        codes, scale = ref.quantize(plain[4][:n])
+        assert torch.equal(ref.values(out[4].t[:n]), codes) and torch.equal(out[5].t[:n], scale)
+        assert torch.all(out[4].t[n:] == 0x5A)
+        most = int(plain[0].max())
+        before = out[4].t.clone()
+        small = N.make_shape(T, H, E, k, 16, capacity=most - 1)
+        N.moe_dispatch_fp8_block(small, x, ids, *(o.t for o in out), ws.t)
+        assert N.moe_status_read(ws.t) in (N.MOE_ERR_CAPACITY, N.MOE_ERR_INVALID_ROUTE)
+        assert torch.equal(out[4].t, before) and torch.equal(out[0].t, plain[0])
+
+
 def test_dispatch_extremes():
     """The largest values, subnormals, rounding ties, and blocks that are not finite."""
     T, H = 6, 400
