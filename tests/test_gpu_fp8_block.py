@@ -465,3 +465,58 @@ def test_layer_over_capacity_leaves_out_as_it_was():
     ids[50:60] = 1
     N.moe_layer_fp8_block(*args)
     assert N.moe_status_read(ws) == N.MOE_OK and not torch.any(torch.all(out == 3, 1))
+
+
+@pytest.mark.parametrize("act", ["swiglu", "relu2"])
+@pytest.mark.parametrize("size", [(1, 1024, 240, 9, 400), (5, 272, 7, 4, 144), (10, 128, 64, 32, 128), (64, 144, 1024, 5, 64),
+                                  (11, 128, 64, 32, 128)], ids=str)
+def test_small_layer_with_repeated_and_invalid_ids(size, act):
+    """Up to 320 pairs the up projection counts its buckets from the ids: as the dispatch does,
+    over capacity, and on one workspace with calls before."""
+    T, H, E, k, I = size
+    d = layer_inputs(T, H, E, k, I, act, 11)
+    kind = N.MOE_ACT_SWIGLU if act == "swiglu" else N.MOE_ACT_RELU2
+    shape, tight = N.make_shape(T, H, E, k, I, kind), N.make_shape(T, H, E, k, I, kind, capacity=1)
+    ws, ws2 = guarded_workspace(shape), N.workspace(shape, dev())
+    w = torch.rand(T, k, generator=gen(12), device=dev())
+    out = torch.empty((T, H), dtype=BF16, device=dev())
+    g = torch.Generator().manual_seed(13)
+    for round_ in range(3):
+        ids = torch.randint(-1, E + 1, (T, k), generator=g, dtype=I32)
+        if round_ == 2:
+            ids[:, 0] = E - 1                                    # a bucket of all tokens
+            ids[0] = E - 1
+        ids = ids.to(dev())
+        call = lambda s: N.moe_layer_fp8_block(s, None, ids, w, d["x"], d["w13"], d["w13_scale"], d["w2"], d["w2_scale"],
+                                               out, ws.t)
+        call(shape)
+        status = N.moe_status_read(ws.t)
+        assert torch.equal(out.view(torch.int16), stages(shape, d, ids, w, None, ws2)[0].view(torch.int16)) and ws.intact()
+        assert status == N.moe_status_read(ws2)
+        if round_ == 2 and T > 1:
+            out.fill_(3.0)
+            call(tight)
+            assert N.moe_status_read(ws.t) != N.MOE_OK and torch.all(out == 3) and ws.intact()
+
+
+def test_small_layer_takes_weights_and_ids_written_just_before():
+    """The layer's kernels start while earlier ones run: what those write is seen all the same."""
+    T, H, E, k, I = 2, 1024, 16, 3, 512
+    d = layer_inputs(T, H, E, k, I, "relu2", 14)
+    shape = N.make_shape(T, H, E, k, I, N.MOE_ACT_RELU2)
+    ws, w = N.workspace(shape, dev()), torch.ones((T, k), device=dev())
+    sets, want = [], []
+    for i in range(2):
+        e = layer_inputs(T, H, E, k, I, "relu2", 15 + i)
+        ids = torch.stack([torch.randperm(E, generator=torch.Generator().manual_seed(i))[:k] for _ in range(T)]).to(I32).to(dev())
+        sets.append((e["w13"], e["w2"], ids))
+        want.append(stages(shape, dict(d, w13=e["w13"], w2=e["w2"]), ids, w, None, ws)[0])
+    w13, w2, ids = (t.clone() for t in sets[0])
+    outs = [torch.empty((T, H), dtype=BF16, device=dev()) for _ in range(60)]
+    for i, out in enumerate(outs):
+        for a, b in zip((w13, w2, ids), sets[i % 2]):
+            a.copy_(b)
+        N.moe_layer_fp8_block(shape, None, ids, w, d["x"], w13, d["w13_scale"], w2, d["w2_scale"], out, ws)
+    assert N.moe_status_read(ws) == N.MOE_OK
+    for i, out in enumerate(outs):
+        assert torch.equal(out.view(torch.int16), want[i % 2].view(torch.int16)), i
