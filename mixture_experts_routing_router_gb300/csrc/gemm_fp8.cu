@@ -23,7 +23,7 @@
 // each, of which 175 are latency) with their multiply-adds and 250 around them: 900 to 1000
 // cycles a step.  Next comes shared memory: 48 KiB brought and 48 KiB read a step, 768 cycles
 // at 128 bytes a cycle (without the weights' loads a call takes 869 us of 902).  Measured
-// and not kept: CTA pairs (M 256; half the shared-memory traffic, but the round trip
+// and not kept: CTA pairs (M 256; two thirds of the shared-memory traffic, but the round trip
 // crosses SMs: 2 to 8 % slower), accumulators of one block each (up to 30 % slower), 16 or
 // 32 columns a read, scales brought by warps of their own, a group's rest of at most 64
 // rows with the operands swapped (three quarters of a wide tile's time, and the larger

@@ -18,9 +18,9 @@
 // selected key against the next one -- is decided by more than that; a token where one
 // is not (about one in a thousand with random logits) is selected again from the
 // defined keys: the winners next to one another among themselves, all experts where the
-// groups are in doubt.  Once in a call (1023 tokens x 160, softmax: 4.5 us without) that adds 3 us, and
-// 5.5 for all experts; in double, without the pairs of floats of route_df.cuh, 10 and more.
-// Two experts of equal logit and bias have equal keys either way.
+// groups are in doubt.  Once in a call (1023 tokens x 160, softmax: 4.5 us without) that
+// adds 3 us, and 5.5 for all experts; in double, without the pairs of floats of
+// route_df.cuh, 10 and more.  Two experts of equal logit and bias have equal keys either way.
 #include "common.cuh"
 #include "route_df.cuh"
 #include "route_warp.cuh"
