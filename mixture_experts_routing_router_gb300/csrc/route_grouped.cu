@@ -320,9 +320,24 @@ route_grouped_kernel(int T, int E, int k, const moe_router r, const float* __res
             if (!__any_sync(kAll, doubt)) break;
             // equal logits with equal biases have equal keys: the lower index came first
             const int next_e = __shfl_down_sync(kAll, sel_e, 1);
-            doubt = doubt && !(__ldg(row + sel_e) == __ldg(row + next_e) &&
-                               (!bias || __ldg(bias + sel_e) == __ldg(bias + next_e)));
-            if (!__any_sync(kAll, doubt)) break;
+            const bool equal = doubt && __ldg(row + sel_e) == __ldg(row + next_e) &&
+                               (!bias || __ldg(bias + sel_e) == __ldg(bias + next_e));
+            if (!__any_sync(kAll, doubt && !equal)) {
+                // Between two that are chosen that settles it.  An equal of the last one that is not
+                // chosen says nothing of those behind it: whatever else is near has to be its equal too.
+                if (!((__ballot_sync(kAll, doubt) >> (k - 1)) & 1u)) break;
+                const int last_e = __shfl_sync(kAll, sel_e, k - 1);
+                const float last = route_unkey(__shfl_sync(kAll, my_key, k - 1));
+                const float last_x = __ldg(row + last_e), last_b = bias ? __ldg(bias + last_e) : 0.f;
+                bool other = false;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const bool left = !((gone >> i) & 1u) && key[i] > -INFINITY;
+                    if (left && !(last - key[i] > key_margin(margin, fmaxf(fabsf(last), fabsf(key[i])))))
+                        other = other || __ldg(row + lane + 32 * i) != last_x || b[i] != last_b;
+                }
+                if (!__any_sync(kAll, other)) break;
+            }
             bool clear;                                               // the last winner is clearly below the others
             for (;;) {
                 const float a = route_unkey(__shfl_sync(kAll, my_key, count - 2)), c = route_unkey(__shfl_sync(kAll, my_key, count - 1));
