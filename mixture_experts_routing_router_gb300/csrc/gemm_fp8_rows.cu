@@ -41,7 +41,9 @@ template <int NSUB, int NB>
 struct RCfg {
     static constexpr int STAGE_BYTES = NSUB * F_BOX + NB * 128;
     static constexpr int STAGES = 192 * 1024 / STAGE_BYTES < R_MAX_STAGES ? 192 * 1024 / STAGE_BYTES : R_MAX_STAGES;
-    static constexpr bool PAIR = NSUB == 1 && NB == 16;               // at most 102 registers, and short stages
+    // two blocks an SM: short stages, and at most 96 registers (a warp's come in eights a
+    // thread: 20 warps at 104 would take 66560), which the launch bounds hold
+    static constexpr bool PAIR = NSUB == 1 && NB == 16;
     static constexpr int ACC_COLS = NSUB * NB;
     static constexpr int ACCS = 512 / ACC_COLS < R_MAX_ACCS ? 512 / ACC_COLS : R_MAX_ACCS;
     static constexpr uint32_t TMEM_COLS = ACCS * ACC_COLS;            // a power of two
@@ -106,7 +108,7 @@ __device__ __forceinline__ int r_tile_list(const FParams& p, int* prefix, int* s
 }
 
 template <int MODE, int NSUB, int NB>
-__global__ void __launch_bounds__(R_THREADS, 1)
+__global__ void __launch_bounds__(R_THREADS, RCfg<NSUB, NB>::PAIR ? 2 : 1)
 fp8_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, const FParams p,
                 const int early) {
     using C = RCfg<NSUB, NB>;
