@@ -218,14 +218,15 @@ def quantize_blocks_fp8(w: torch.Tensor):
     """Input preparation for block-scaled FP8 expert weights: each block of 128 x 128
     of ``w`` [..., rows, K] (cut off at the edges) becomes E4M3 codes (torch's
     round-to-nearest float8_e4m3fn conversion) of w / scale with
-    scale = max|block| / 448 (1 for an all-zero block).
+    scale = max|block| / 448, 2^-126 at least (below that a scale loses its digits, and 0
+    would divide zeros by it; 1 for an all-zero block).
     -> (codes uint8 [..., rows, K], scale float32 [..., ceil(rows/128), ceil(K/128)])."""
     rows, K = w.shape[-2:]
     nr, nk = (rows + 127) // 128, (K + 127) // 128
     wf = torch.nn.functional.pad(w.float(), (0, nk * 128 - K, 0, nr * 128 - rows))
     blk = wf.unflatten(-1, (nk, 128)).unflatten(-3, (nr, 128))       # [..., nr, 128, nk, 128]
     amax = blk.abs().amax(dim=(-3, -1))
-    scale = torch.where(amax > 0, amax / 448.0, torch.ones_like(amax))
+    scale = torch.where(amax > 0, (amax / 448.0).clamp(min=2.0 ** -126), torch.ones_like(amax))
     codes = (blk / scale[..., :, None, :, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
     codes = codes.flatten(-2).flatten(-3, -2)[..., :rows, :K]
     return codes.contiguous(), scale.contiguous()

@@ -40,3 +40,15 @@ def test_expert_weights_have_a_grid_per_matrix():
     assert (up - a[80:].double()).abs().max() <= 2.0 ** -4 * a.abs().max().double()
     down = values(d["w2"][2]) * spread_cols(spread_rows(d["s2"][2], 144), 80)
     assert (down - b.double()).abs().max() <= 2.0 ** -4 * b.abs().max().double()
+
+
+@pytest.mark.parametrize("amax", [2.0 ** -149, 2.0 ** -140, 2.0 ** -126, 2.0 ** -118, 2.0 ** -117])
+def test_blocks_of_tiny_weights(amax):
+    """Largest values at which max / 448 is below FP32's normal range, zeros among them."""
+    w = torch.zeros(130, 144)
+    w[0, 0], w[5, 7], w[129, 143] = amax, -0.75 * amax, 0.5 * amax
+    codes, scale = synth.quantize_blocks_fp8(w)
+    v = values(codes) * spread_cols(spread_rows(scale, 130), 144)
+    s = spread_cols(spread_rows(scale, 130), 144)
+    assert ((v - w.double()).abs() <= 2.0 ** -4 * (1 + 2.0 ** -18) * w.double().abs() + 2.0 ** -10 * s).all()
+    assert not codes[w == 0].any()
