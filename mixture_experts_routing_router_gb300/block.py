@@ -128,6 +128,8 @@ class MoEBlock(torch.nn.Module):
     then has a buffer ``route_bias`` [experts] FP32, zeros at first, that only selects: it
     has no gradient, and a program that balances its experts adds to it between steps."""
 
+    router = None        # of blocks that were pickled whole before there was one, too
+
     def __init__(self, hidden, experts, top_k, inter, act=N.MOE_ACT_SWIGLU, eps=1e-5, device="cuda", generator=None,
                  router=None):
         super().__init__()
