@@ -351,10 +351,13 @@ MOE_API moe_status moe_layer_nvfp4(const moe_shape* shape, const float* logits, 
  *                    [E, P, nb(I), nb(H)], P = 2 for SwiGLU (gate, then up, each with
  *                    blocks of its own) and 1 for ReLU^2; w2 [E, H, I], [E, nb(H), nb(I)].
  * Rows are quantized by the library: for a block of a row with a = max(max|x|, 2^-100),
- * scale = a / 448 and code = the E4M3 value nearest 448 x / a (ties to even); a block
+ * scale = a / 448 and code = the E4M3 value nearest 448 x / a (ties to even; for h, whose
+ * values are FP32, of the quotient as FP32 has it, to a few units in its last place); a block
  * with a NaN or an infinity gets NaN codes and a NaN scale, and its row's outputs are NaN.
  * NaN codes in the weights make the outputs that they reach NaN.
- * Sums are FP32: each 128-wide block's sum of products, times both scales, added up.
+ * Sums are FP32: each 128-wide block's sum of products, times the product of both scales
+ * (FP32, taken first: where it overflows the outputs are not finite, even if the block's
+ * products are 0; below 2^-126 it loses digits), added up.
  * A row's results do not depend on which rows share its call or its bucket.
  * Host errors: MOE_ERR_UNSUPPORTED when shape->shared > 0; MOE_ERR_INVALID_ARG when
  * hidden or inter is not a multiple of 16 or a pointer is not 16-byte aligned.

@@ -93,7 +93,7 @@ scatter_fp8_kernel(int T, int H, int k, int E, const uint16_t* __restrict__ x, c
 
 // The whole dispatch of up to kSmallPairs pairs in one launch: every block counts all pairs
 // (and those before its own tokens') in shared memory, so that none waits for another;
-// then it places and quantizes its tokens.  1024 tokens x 2048, k = 6, 64 experts: 9.3
+// then it places and quantizes its tokens.  1024 tokens x 2048, k = 6, 64 experts: 8.7
 // us, against 14.2 of clearing the look-back flags, counting and scattering in turn.
 // Stable, and what is valid, as count_kernel and scatter_kernel have it: the slot of pair p
 // is offsets[e] + the valid pairs of e before p.

@@ -4,7 +4,8 @@
 //   scale = a / 448,   code = the E4M3 value nearest 448 x / a (ties to even).
 // 448 x / a is taken as (0.875 x) / (a / 512): no product here can overflow, and for
 // BF16 x both sides are exact, so the quotient is a tie between two codes in FP32 only
-// if it is one.  A block with a NaN or an infinity has the scale NaN and the codes NaN.
+// if it is one.  For FP32 x (the up projection's results) 0.875 x is rounded first, so a
+// quotient within a few 2^-24 of a border may fall to either side.  A block with a NaN or an infinity has the scale NaN and the codes NaN.
 #pragma once
 
 #include "common.cuh"
@@ -54,7 +55,7 @@ __device__ __forceinline__ uint32_t fp8_quant4(const Fp8Quant& q, float a, float
 
 // Grouped product of E4M3 rows and E4M3 weights:
 //   y[r, n] = sum_b a_scale[r, b] w_scale[g, n / 128, b] sum_{c in block b} a[r, c] w[g, n, c]
-// over the rows r of group g, FP32 sums; then plain BF16, or an activation quantized
+// over the rows r of group g, FP32 sums (the scales' product is taken first, in FP32); then plain BF16, or an activation quantized
 // again (SwiGLU: the weights' gate rows, then their up rows, each with blocks of its own).
 struct Fp8Problem {
     int mode;                                  // kGemmSwiGLU / kGemmReLU2 / kGemmPlain

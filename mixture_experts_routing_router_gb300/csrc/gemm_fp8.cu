@@ -93,7 +93,7 @@ __device__ __forceinline__ void store_rows(uint8_t* stg, const uint32_t (&u)[16]
     }
 }
 
-// Rows that the TMA loads of a CTA with `rows` rows of the tile bring: boxes of 8, 32 or
+// Rows that the TMA loads of a tile with `rows` rows bring: boxes of 8, 32 or
 // 128 rows.  The rows of the slot past them keep what they hold, which reaches only
 // output rows that are not stored.
 __device__ __forceinline__ int f_box(int rows) { return rows <= 8 ? 8 : rows <= 96 ? 32 : 128; }
@@ -150,7 +150,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");         // 128 x 40 + 256 x 232 = 384 x 168 registers
         if (warp == 0) {
-            // ---------------- TMA producer (both CTAs of a pair) ----------------
+            // ---------------- TMA producer ----------------
             if (lane == 0) {
                 int stage = 0;
                 uint32_t ph = 0;
@@ -228,7 +228,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         // ---------------- adding up, activation, store (warps 4..11) ----------------
         const int q = warp & 3, hf = (warp - 4) >> 2;
-        const int rl = 32 * q + lane;                                 // row of this CTA's part of the tile
+        const int rl = 32 * q + lane;                                 // row of the tile
         uint8_t* stg = store + (size_t)(warp - 4) * F_STORE;
         int acc = 0, parity = 0;
         uint32_t aph = 0;

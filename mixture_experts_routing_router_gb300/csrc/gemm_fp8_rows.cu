@@ -11,9 +11,10 @@
 //
 // Bound by HBM: 8 tokens, 64 experts, 7168 x 2048: up 179 us (6.7 TB/s), down 92 (6.6); 16
 // tokens with 240 experts, 1024 x 1536: 5.4 to 5.7 TB/s, what is left being the first loads
-// and the last tile's epilogue.  The row kernel takes 49 us where these two take 41.  Above
-// 64 tokens groups are small only by chance, and this kernel's narrow tiles lose (200 tokens:
-// up 66 -> 75 us).
+// and the last tile's epilogue.  The row kernel takes 49 us where these two take 41.  Taken
+// up to 64 tokens, the host's bound on a group's rows.  More tokens over many experts can
+// have as few rows a group; the one such point that was compared (200 tokens: up 66 us with
+// the row kernel, 75 with this one) went to the row kernel, others are not measured.
 //
 // Roles: warp 0 TMA, warp 1 MMA, warps 2..9 add up and store: warp w owns TMEM lanes
 // 32 (w % 4) .. +31 and rows h NB / 2 .. of the tile (h = (w - 2) / 4).  For SwiGLU the two

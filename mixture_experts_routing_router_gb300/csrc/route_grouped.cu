@@ -16,11 +16,17 @@
 // therefore works on FP32 keys with a bound on their error (key_margin) and checks
 // that every comparison the result hangs on -- chosen against other groups, each
 // selected key against the next one -- is decided by more than that; a token where one
-// is not (about one in a thousand with random logits) is selected again from the
-// defined keys: the winners next to one another among themselves, all experts where the
-// groups are in doubt.  Once in a call (1023 tokens x 160, softmax: 4.5 us without) that
-// adds 3 us, and 5.5 for all experts; in double, without the pairs of floats of
-// route_df.cuh, 10 and more.  Two experts of equal logit and bias have equal keys either way.
+// is not (about one in a thousand with logits of N(0, 1), more with peaked ones: the margin
+// is absolute) is selected again from the defined keys: the winners next to one another
+// among themselves, all experts where the groups are in doubt.  Once in a call (1023 tokens
+// x 160, softmax: 4.5 us without) that adds 3 us, and 5.5 for all experts; in double,
+// without the pairs of floats of route_df.cuh, 10 and more.  Batches of such tokens
+// (16384 x 256, k = 8): BF16-valued softmax logits of N(0, 16) 32 us without groups and 39
+// with 4 of 8 (30 for N(0, 1)); all logits equal, so that every token's groups tie, 75 us
+// with sigmoid scores and 105 with softmax.
+// Two experts of equal logit and bias have equal keys either way, which decides between
+// two that are both chosen, and at the last place if all that is near is equal (all logits
+// equal, one group: 23 us with sigmoid scores, 25 with softmax).
 #include "common.cuh"
 #include "route_df.cuh"
 #include "route_warp.cuh"
@@ -141,9 +147,10 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
 }
 
 // EPL = experts per lane (E <= 32 * EPL; FULL: equal); lane l holds experts l, l + 32, ...
-// Bound by instructions (16384 tokens of 256 experts, 8 groups: 27 us; selects
+// Bound by the latency of a token's dependent steps (16384 tokens of 256 experts, 8 groups:
+// 26.5 to 29 us, 1141 instructions a token at 48 % of the issue slots; selects
 // instead of branches, and what a warp's tokens share kept in registers -- biases, a
-// key's place in shared memory and its group -- took it from 1500 to about 700 a token).
+// key's place in shared memory and its group -- took it there from 1500 instructions).
 // A lane keeps its two best candidates, so that most rounds of warp-wide argmax need no
 // pass over its keys; the comparisons are checked once, side by side, after the rounds.
 template <int EPL, bool FULL>
